@@ -423,6 +423,105 @@ LA_EXPORT la_status la_backward_sp_dkdv(const void *q, const void *k, const void
                                         void *workspace, size_t workspace_bytes,
                                         la_stream_t stream);
 
+/*
+ * Gated linear attention: the causal recurrence with a gate per token and
+ * head that the data decide (the "gating" of "Efficient Transformers Survey",
+ * Common Confusions, "Watch Out", where la_*_decay take a constant), and no
+ * denominator:
+ *     S_t = a_t S_{t-1} + k_t v_t^T,   o_t = scale * S_t^T q_t,
+ *     a_t = exp(log_gate_t).
+ * q and k are taken as they are, of either sign (no feature map); la_group_norm
+ * below is the norm such an output takes in the denominator's place.
+ *
+ * q, o, dO, dq: [B, H, N, D]; k, v, dk, dv: [B, Hkv, N, D]; log_gate and
+ * dlog_gate: [B, Hkv, N], which need no more alignment than their elements;
+ * all of dtype `dt`.  Hkv divides H, and query head h
+ * reads key/value head h / (H / Hkv), as in la_forward_gqa.  S_in (may be
+ * NULL: zero) is the state before the first token and S_out (may be NULL)
+ * receives the state after the last, float32 [B, Hkv, D, D] (row = key
+ * feature), so a sequence can be taken in pieces and handed to
+ * la_decode_step_gated; they must not overlap.
+ *
+ * log_gate is the natural logarithm of a gate in [0, 1]: at most 0, and -inf
+ * drops the state (a packed document's first token).  Values above 0 are not
+ * looked for; the state then grows as the recurrence says, until float32
+ * overflows.  Sums of log gates are held in 64 bits.  A gate below 2^-160 is
+ * taken as 0.  dlog_gate is the gradient with respect to log_gate (0 where
+ * the gate is 0).
+ *
+ * la_backward_gated: gradients of sum(dO * O) + sum(dS_out * S_out) with
+ * respect to q, k, v, log_gate and S_in (dS_in, may be NULL).  dS_out may be
+ * NULL (zero).  The gradients must not overlap the inputs or each other.  The
+ * gradients of shared heads are added within the kernels, in a fixed order;
+ * every call is bitwise repeatable.
+ *
+ * Types and sizes as la_forward's.  bf16 inputs are read exactly; the state
+ * and all sums are float32.  Workspace: la_workspace_size_gated (0 for
+ * arguments that the calls refuse); two calls that may overlap (two streams,
+ * two captured graphs) need one each.  N = 0 copies S_in to S_out, and dS_out
+ * to dS_in.  Errors as la_forward.
+ */
+LA_EXPORT size_t la_workspace_size_gated(la_op op, int64_t B, int64_t H, int64_t Hkv, int64_t N,
+                                         int64_t D, la_dtype dt);
+LA_EXPORT la_status la_forward_gated(const void *q, const void *k, const void *v,
+                                     const void *log_gate, void *o, const float *S_in,
+                                     float *S_out, float scale, int64_t B, int64_t H, int64_t Hkv,
+                                     int64_t N, int64_t D, la_dtype dt, void *workspace,
+                                     size_t workspace_bytes, la_stream_t stream);
+LA_EXPORT la_status la_backward_gated(const void *q, const void *k, const void *v,
+                                      const void *log_gate, const void *dO, const float *S_in,
+                                      const float *dS_out, void *dq, void *dk, void *dv,
+                                      void *dlog_gate, float *dS_in, float scale, int64_t B,
+                                      int64_t H, int64_t Hkv, int64_t N, int64_t D, la_dtype dt,
+                                      void *workspace, size_t workspace_bytes,
+                                      la_stream_t stream);
+
+/*
+ * One step of the same recurrence in place, for every (b, h): S float32
+ * [B, Hkv, D, D] becomes exp(log_gate) S + k v^T, then o = scale * S^T q.
+ * q, o: [B, H, D]; k, v: [B, Hkv, D]; log_gate: [B, Hkv].  o must not alias
+ * an input.  No workspace.  Errors as la_decode_step.
+ */
+LA_EXPORT la_status la_decode_step_gated(float *S, const void *q, const void *k, const void *v,
+                                         const void *log_gate, void *o, float scale, int64_t B,
+                                         int64_t H, int64_t Hkv, int64_t D, la_dtype dt,
+                                         la_stream_t stream);
+
+typedef enum la_act {
+    LA_ACT_IDENTITY = 0,  /* act(x) = x */
+    LA_ACT_SILU = 1       /* act(x) = x / (1 + exp(-x)) */
+} la_act;
+
+/*
+ * Group norm of an attention output, one group per head and token, with an
+ * activation, written channels last.  x: [B, H, N, D]; y: [B, N, H*D], both
+ * of dtype `dt`.  With c = h*D + d and x_hat the row x[b, h, n, :] less its
+ * mean over sqrt(its variance + eps), m = weight_c x_hat + bias_c:
+ *     y[b, n, c] = m * act(gate[b, n, c])   with a gate ([B, N, H*D], `dt`)
+ *     y[b, n, c] = act(m)                   with gate = NULL
+ * weight: float32 [H*D]; bias: float32 [H*D] or NULL (zero).  eps > 0 and
+ * finite (else LA_ERR_INVALID_ARG).  Statistics are float32; y is rounded
+ * once.  D: 16, 32, 64 or 128; H*D up to 2^24.  y must not overlap the inputs.
+ *
+ * la_group_norm_backward: gradients of sum(dy * y): dx [B, H, N, D], dgate
+ * [B, N, H*D] (required exactly when gate is given), dweight float32 [H*D],
+ * dbias float32 [H*D] (may be NULL).  The statistics are computed again from
+ * x.  The channel sums are added in a fixed order.  Workspace:
+ * la_workspace_size_group_norm.  N = 0 writes zeros to dweight and dbias.
+ */
+LA_EXPORT la_status la_group_norm(const void *x, const void *gate, const float *weight,
+                                  const float *bias, void *y, float eps, la_act act, int64_t B,
+                                  int64_t H, int64_t N, int64_t D, la_dtype dt,
+                                  la_stream_t stream);
+LA_EXPORT size_t la_workspace_size_group_norm(int64_t B, int64_t H, int64_t N, int64_t D,
+                                              la_dtype dt);
+LA_EXPORT la_status la_group_norm_backward(const void *x, const void *gate, const float *weight,
+                                           const float *bias, const void *dy, void *dx,
+                                           void *dgate, float *dweight, float *dbias, float eps,
+                                           la_act act, int64_t B, int64_t H, int64_t N, int64_t D,
+                                           la_dtype dt, void *workspace, size_t workspace_bytes,
+                                           la_stream_t stream);
+
 /* Static English text for a status code (never NULL). */
 LA_EXPORT const char *la_status_string(la_status status);
 

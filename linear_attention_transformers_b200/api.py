@@ -14,6 +14,11 @@ raises ``RuntimeError``.
     la_forward_decay(q, k, v, gamma, phi="elu1", ...)        -> o [, S, z]  (causal)
     la_backward_decay(q, k, v, dO, gamma, phi="elu1", ...)   -> dq, dk, dv
     la_decode_step_decay(S, z, q, k, v, gamma, ...)          -> o   (S, z in place)
+    la_forward_gated(q, k, v, log_gate, scale=1.0, ...)      -> o [, S]  (a gate per token and head)
+    la_backward_gated(q, k, v, log_gate, dO, scale=1.0, ...) -> dq, dk, dv, dlog_gate [, dS_in]
+    la_decode_step_gated(S, q, k, v, log_gate, scale=1.0)    -> o   (S in place)
+    la_group_norm(x, weight, bias, gate, act, eps)           -> y   (channels last)
+    la_group_norm_backward(x, weight, dy, bias, gate, ...)   -> dx, dweight, dbias, dgate
     la_favor_features(x, omega)                              -> phi(x)  (Performer FAVOR+)
     la_favor_features_backward(x, omega, dphi)               -> dx
     la_forward_mv / la_backward_mv(q, k, v[, dO])            features of length m != D
@@ -22,11 +27,17 @@ raises ``RuntimeError``.
                                                               sequence split across ranks)
     la_get_device_error(stream=None)                         -> raises on a device timeout
     LinearAttention.apply(q, k, v, causal, phi)              -> o   (torch autograd)
+    GatedLinearAttention.apply(q, k, v, log_gate, scale, S_in, return_state)
+                                                             -> o or (o, S)   (torch autograd)
+    HeadGroupNorm.apply(x, weight, bias, gate, act, eps)     -> y   (torch autograd)
 
 k and v may have fewer heads than q (grouped-query / multi-query attention:
 Hkv key/value heads shared by groups of H / Hkv query heads); the group size
 is read from their shapes.  The *_decay calls take one decay factor per head
-(gamma, H host values in [0, 1]): S_i = gamma S_{i-1} + phi(k_i) v_i^T.
+(gamma, H host values in [0, 1]): S_i = gamma S_{i-1} + phi(k_i) v_i^T.  The
+*_gated calls take the logarithm of a gate per token and head from a tensor,
+with its gradient: S_t = exp(log_gate_t) S_{t-1} + k_t v_t^T, o_t = scale
+S_t^T q_t, without a denominator.
 With phi="identity" q and k are taken as feature vectors already (for
 example la_favor_features(q, omega)), and the backward returns their
 gradients.
@@ -52,6 +63,7 @@ LA_OP_FORWARD = 0
 LA_OP_BACKWARD = 1
 PHI = {"elu1": 0, "relu_eps": 1, "identity": 2, 0: 0, 1: 1, 2: 2}
 DTYPE = {torch.float32: LA_F32, torch.bfloat16: LA_BF16}
+ACT = {"identity": 0, "silu": 1}
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "liblinattn.so")
@@ -120,6 +132,25 @@ def load_library(path: str | None = None):
         lib.la_backward_decay.restype = ci
         lib.la_decode_step_decay.argtypes = [vp, vp, vp, vp, vp, vp, fp, i64, i64, i64, ci, ci, vp]
         lib.la_decode_step_decay.restype = ci
+        cf = ctypes.c_float
+        lib.la_workspace_size_gated.argtypes = [ci, i64, i64, i64, i64, i64, ci]
+        lib.la_workspace_size_gated.restype = sz
+        lib.la_forward_gated.argtypes = [vp, vp, vp, vp, vp, vp, vp, cf, i64, i64, i64, i64, i64,
+                                         ci, vp, sz, vp]
+        lib.la_forward_gated.restype = ci
+        lib.la_backward_gated.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, cf, i64,
+                                          i64, i64, i64, i64, ci, vp, sz, vp]
+        lib.la_backward_gated.restype = ci
+        lib.la_decode_step_gated.argtypes = [vp, vp, vp, vp, vp, vp, cf, i64, i64, i64, i64, ci,
+                                             vp]
+        lib.la_decode_step_gated.restype = ci
+        lib.la_group_norm.argtypes = [vp, vp, vp, vp, vp, cf, ci, i64, i64, i64, i64, ci, vp]
+        lib.la_group_norm.restype = ci
+        lib.la_workspace_size_group_norm.argtypes = [i64, i64, i64, i64, ci]
+        lib.la_workspace_size_group_norm.restype = sz
+        lib.la_group_norm_backward.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, cf, ci, i64,
+                                               i64, i64, i64, ci, vp, sz, vp]
+        lib.la_group_norm_backward.restype = ci
         lib.la_favor_features.argtypes = [vp, vp, vp, i64, i64, i64, i64, i64, ci, vp]
         lib.la_favor_features.restype = ci
         lib.la_favor_features_backward.argtypes = [vp, vp, vp, vp, i64, i64, i64, i64, i64, ci,
@@ -486,6 +517,217 @@ def la_decode_step_decay(S, z, q, k, v, gamma, phi="elu1", o=None, stream=None):
     return o
 
 
+# ------------------------------------------- gated LA and the head-row norm
+class _LaunchOn:
+    """The device of ``t`` and the stream to launch on: the caller's, or the
+    device's current one.  Within it torch allocates from that stream's pool,
+    so a workspace that is dropped when the call returns is only reused behind
+    the kernels that read it."""
+
+    __slots__ = ("_ctx",)
+
+    def __init__(self, t, stream):
+        self._ctx = None
+        if stream is not None:
+            if stream.device != t.device:
+                raise ValueError(f"stream is on {stream.device}, the tensors on {t.device}")
+            self._ctx = torch.cuda.stream(stream)
+        elif t.device.index != torch.cuda.current_device():
+            self._ctx = torch.cuda.device(t.device)
+
+    def __enter__(self):
+        if self._ctx is not None:
+            self._ctx.__enter__()
+        return torch.cuda.current_stream().cuda_stream
+
+    def __exit__(self, *exc):
+        if self._ctx is not None:
+            return self._ctx.__exit__(*exc)
+        return None
+
+
+def _check_like(name, what, t, ref, shape, dtype=None):
+    if (t.dtype != (dtype or ref.dtype) or tuple(t.shape) != tuple(shape)
+            or t.device != ref.device or not t.is_contiguous()):
+        raise ValueError(f"{name}: {what} must be contiguous {dtype or ref.dtype} {tuple(shape)} "
+                         f"on {ref.device}")
+
+
+def _scratch(name, need, workspace, device):
+    if workspace is None:
+        return (torch.empty(need, dtype=torch.uint8, device=device), need) if need else (None, 0)
+    have = workspace.numel() * workspace.element_size()
+    if workspace.device != device or not workspace.is_contiguous() or have < need:
+        raise ValueError(f"{name}: workspace must be contiguous, on {device} and of at least "
+                         f"{need} bytes")
+    return workspace, have
+
+
+def la_workspace_size_gated(op: int, B: int, H: int, N: int, D: int, dtype: torch.dtype,
+                            Hkv: int | None = None) -> int:
+    return int(load_library().la_workspace_size_gated(int(op), B, H, H if Hkv is None else Hkv, N,
+                                                      D, DTYPE[dtype]))
+
+
+def la_forward_gated(q, k, v, log_gate, scale: float = 1.0, S_in=None, o=None,
+                     return_state=False, S_out=None, workspace=None, stream=None):
+    """o = scale S_t^T q_t for S_t = exp(log_gate_t) S_{t-1} + k_t v_t^T.
+
+    q [B, H, N, D]; k, v [B, Hkv, N, D]; log_gate [B, Hkv, N], at most 0 (-inf
+    drops the state), of q's dtype.  ``S_in``: the float32 state [B, Hkv, D, D]
+    before the first token (None: zero).  ``return_state``: also return the
+    state after the last token, in ``S_out`` if given.
+    """
+    lib = load_library()
+    _check_qkv("la_forward_gated", q)
+    if q.dim() != 4:
+        raise ValueError("la_forward_gated: q must be [B, H, N, D], k and v [B, Hkv, N, D]")
+    Hkv = _check_kv("la_forward_gated", q, k, v)
+    B, H, N, D = q.shape
+    _check_like("la_forward_gated", "log_gate", log_gate, q, (B, Hkv, N))
+    for what, t in (("S_in", S_in), ("S_out", S_out)):
+        if t is not None:
+            _check_like("la_forward_gated", what, t, q, (B, Hkv, D, D), torch.float32)
+    if o is not None:
+        _check_qkv("la_forward_gated", q, o)
+    with _LaunchOn(q, stream) as handle:
+        if o is None:
+            o = torch.empty_like(q)
+        if S_out is None and return_state:
+            S_out = torch.empty((B, Hkv, D, D), dtype=torch.float32, device=q.device)
+        ws, ws_bytes = _scratch("la_forward_gated", lib.la_workspace_size_gated(
+            LA_OP_FORWARD, B, H, Hkv, N, D, DTYPE[q.dtype]), workspace, q.device)
+        st = lib.la_forward_gated(_ptr(q), _ptr(k), _ptr(v), _ptr(log_gate), _ptr(o), _ptr(S_in),
+                                  _ptr(S_out), scale, B, H, Hkv, N, D, DTYPE[q.dtype], _ptr(ws),
+                                  ws_bytes, handle)
+    _check("la_forward_gated", st)
+    return (o, S_out) if return_state else o
+
+
+def la_backward_gated(q, k, v, log_gate, dO, scale: float = 1.0, S_in=None, dS_out=None, dq=None,
+                      dk=None, dv=None, dlog_gate=None, return_dstate=False, dS_in=None,
+                      workspace=None, stream=None):
+    """(dq, dk, dv, dlog_gate) of sum(dO * o) + sum(dS_out * S_out) for
+    (o, S_out) = la_forward_gated(q, k, v, log_gate, scale, S_in), and with
+    ``return_dstate`` also the gradient of S_in.  ``dS_out`` None: zero."""
+    lib = load_library()
+    _check_qkv("la_backward_gated", q, dO)
+    if q.dim() != 4:
+        raise ValueError("la_backward_gated: q must be [B, H, N, D], k and v [B, Hkv, N, D]")
+    Hkv = _check_kv("la_backward_gated", q, k, v)
+    B, H, N, D = q.shape
+    _check_like("la_backward_gated", "log_gate", log_gate, q, (B, Hkv, N))
+    for what, t in (("S_in", S_in), ("dS_out", dS_out), ("dS_in", dS_in)):
+        if t is not None:
+            _check_like("la_backward_gated", what, t, q, (B, Hkv, D, D), torch.float32)
+    for what, t, ref in (("dq", dq, q), ("dk", dk, k), ("dv", dv, k), ("dlog_gate", dlog_gate,
+                                                                      log_gate)):
+        if t is not None:
+            _check_like("la_backward_gated", what, t, ref, ref.shape)
+    with _LaunchOn(q, stream) as handle:
+        dq = torch.empty_like(q) if dq is None else dq
+        dk = torch.empty_like(k) if dk is None else dk
+        dv = torch.empty_like(k) if dv is None else dv
+        dlog_gate = torch.empty_like(log_gate) if dlog_gate is None else dlog_gate
+        if dS_in is None and return_dstate:
+            dS_in = torch.empty((B, Hkv, D, D), dtype=torch.float32, device=q.device)
+        ws, ws_bytes = _scratch("la_backward_gated", lib.la_workspace_size_gated(
+            LA_OP_BACKWARD, B, H, Hkv, N, D, DTYPE[q.dtype]), workspace, q.device)
+        st = lib.la_backward_gated(_ptr(q), _ptr(k), _ptr(v), _ptr(log_gate), _ptr(dO),
+                                   _ptr(S_in), _ptr(dS_out), _ptr(dq), _ptr(dk), _ptr(dv),
+                                   _ptr(dlog_gate), _ptr(dS_in), scale, B, H, Hkv, N, D,
+                                   DTYPE[q.dtype], _ptr(ws), ws_bytes, handle)
+    _check("la_backward_gated", st)
+    return (dq, dk, dv, dlog_gate, dS_in) if return_dstate else (dq, dk, dv, dlog_gate)
+
+
+def la_decode_step_gated(S, q, k, v, log_gate, scale: float = 1.0, o=None, stream=None):
+    """One gated step in place: S (float32 [B, Hkv, D, D]) = exp(log_gate) S +
+    k v^T, then o = scale S^T q; q [B, H, D], k, v [B, Hkv, D], log_gate
+    [B, Hkv].  Returns o."""
+    lib = load_library()
+    _check_qkv("la_decode_step_gated", q)
+    if q.dim() != 3:
+        raise ValueError("la_decode_step_gated: q must be [B, H, D], k and v [B, Hkv, D]")
+    Hkv = _check_kv("la_decode_step_gated", q, k, v)
+    B, H, D = q.shape
+    _check_like("la_decode_step_gated", "log_gate", log_gate, q, (B, Hkv))
+    _check_like("la_decode_step_gated", "S", S, q, (B, Hkv, D, D), torch.float32)
+    if o is not None:
+        _check_qkv("la_decode_step_gated", q, o)
+    with _LaunchOn(q, stream) as handle:
+        o = torch.empty_like(q) if o is None else o
+        st = lib.la_decode_step_gated(_ptr(S), _ptr(q), _ptr(k), _ptr(v), _ptr(log_gate), _ptr(o),
+                                      scale, B, H, Hkv, D, DTYPE[q.dtype], handle)
+    _check("la_decode_step_gated", st)
+    return o
+
+
+def _check_norm(name, x, weight, bias, gate, act):
+    _check_qkv(name, x)
+    if x.dim() != 4:
+        raise ValueError(f"{name}: x must be [B, H, N, D]")
+    if act not in ACT:
+        raise ValueError(f"{name}: act must be 'identity' or 'silu', got {act!r}")
+    B, H, N, D = x.shape
+    _check_like(name, "weight", weight, x, (H * D,), torch.float32)
+    if bias is not None:
+        _check_like(name, "bias", bias, x, (H * D,), torch.float32)
+    if gate is not None:
+        _check_like(name, "gate", gate, x, (B, N, H * D))
+    return B, H, N, D
+
+
+def la_group_norm(x, weight, bias=None, gate=None, act="silu", eps: float = 1e-5, y=None,
+                  stream=None):
+    """y [B, N, H*D] (channels last) of x [B, H, N, D], each head's row
+    normalised over its D elements: with m = weight * x_hat + bias, y = m *
+    act(gate), or act(m) without a gate.  weight, bias: float32 [H*D]."""
+    lib = load_library()
+    B, H, N, D = _check_norm("la_group_norm", x, weight, bias, gate, act)
+    if y is not None:
+        _check_like("la_group_norm", "y", y, x, (B, N, H * D))
+    with _LaunchOn(x, stream) as handle:
+        if y is None:
+            y = torch.empty((B, N, H * D), dtype=x.dtype, device=x.device)
+        st = lib.la_group_norm(_ptr(x), _ptr(gate), _ptr(weight), _ptr(bias), _ptr(y), eps,
+                               ACT[act], B, H, N, D, DTYPE[x.dtype], handle)
+    _check("la_group_norm", st)
+    return y
+
+
+def la_group_norm_backward(x, weight, dy, bias=None, gate=None, act="silu", eps: float = 1e-5,
+                           dx=None, dweight=None, dbias=None, dgate=None, workspace=None,
+                           stream=None):
+    """(dx, dweight, dbias, dgate) of sum(dy * y) for y = la_group_norm(x,
+    weight, bias, gate, act, eps); dbias is None without a bias, dgate without
+    a gate."""
+    lib = load_library()
+    B, H, N, D = _check_norm("la_group_norm_backward", x, weight, bias, gate, act)
+    _check_like("la_group_norm_backward", "dy", dy, x, (B, N, H * D))
+    if (bias is None and dbias is not None) or (gate is None and dgate is not None):
+        raise ValueError("la_group_norm_backward: dbias goes with bias, dgate with gate")
+    for what, t, ref in (("dx", dx, x), ("dweight", dweight, weight), ("dbias", dbias, weight),
+                         ("dgate", dgate, dy)):
+        if t is not None:
+            _check_like("la_group_norm_backward", what, t, ref, ref.shape)
+    with _LaunchOn(x, stream) as handle:
+        dx = torch.empty_like(x) if dx is None else dx
+        dweight = torch.empty_like(weight) if dweight is None else dweight
+        if bias is not None and dbias is None:
+            dbias = torch.empty_like(bias)
+        if gate is not None and dgate is None:
+            dgate = torch.empty_like(gate)
+        ws, ws_bytes = _scratch("la_group_norm_backward", lib.la_workspace_size_group_norm(
+            B, H, N, D, DTYPE[x.dtype]), workspace, x.device)
+        st = lib.la_group_norm_backward(_ptr(x), _ptr(gate), _ptr(weight), _ptr(bias), _ptr(dy),
+                                        _ptr(dx), _ptr(dgate), _ptr(dweight), _ptr(dbias), eps,
+                                        ACT[act], B, H, N, D, DTYPE[x.dtype], _ptr(ws), ws_bytes,
+                                        handle)
+    _check("la_group_norm_backward", st)
+    return dx, dweight, dbias, dgate
+
+
 # ------------------------------------------------ Performer FAVOR+ features
 def _check_omega(name, x, omega):
     m = x.shape[-1]
@@ -797,3 +1039,49 @@ class LinearAttention(torch.autograd.Function):
         dq, dk, dv = la_backward(q, k, v, dO.contiguous(), ctx.causal, ctx.phi, o=o, g=g,
                                  phi_q=pq, phi_k=pk)
         return dq, dk, dv, None, None
+
+
+class GatedLinearAttention(torch.autograd.Function):
+    """torch autograd wrapper of la_forward_gated / la_backward_gated: o, or
+    (o, S) with ``return_state``; gradients for q, k, v, log_gate and S_in."""
+
+    @staticmethod
+    def forward(ctx, q, k, v, log_gate, scale=1.0, S_in=None, return_state=False):
+        q, k, v, log_gate = (t.contiguous() for t in (q, k, v, log_gate))
+        S_in = None if S_in is None else S_in.contiguous()
+        ctx.set_materialize_grads(False)
+        ctx.save_for_backward(q, k, v, log_gate, S_in)
+        ctx.scale = float(scale)
+        return la_forward_gated(q, k, v, log_gate, ctx.scale, S_in, return_state=return_state)
+
+    @staticmethod
+    def backward(ctx, dO, dS_out=None):
+        q, k, v, log_gate, S_in = ctx.saved_tensors
+        if dO is None and dS_out is None:
+            return (None,) * 7
+        dO = torch.zeros_like(q) if dO is None else dO.contiguous()
+        dS_out = None if dS_out is None else dS_out.contiguous()
+        want = S_in is not None and ctx.needs_input_grad[5]
+        dq, dk, dv, dlog, *dS = la_backward_gated(q, k, v, log_gate, dO, ctx.scale, S_in, dS_out,
+                                                  return_dstate=want)
+        return dq, dk, dv, dlog, None, dS[0] if want else None, None
+
+
+class HeadGroupNorm(torch.autograd.Function):
+    """torch autograd wrapper of la_group_norm / la_group_norm_backward."""
+
+    @staticmethod
+    def forward(ctx, x, weight, bias=None, gate=None, act="silu", eps=1e-5):
+        x, weight = x.contiguous(), weight.contiguous()
+        bias = None if bias is None else bias.contiguous()
+        gate = None if gate is None else gate.contiguous()
+        ctx.save_for_backward(x, weight, bias, gate)
+        ctx.act, ctx.eps = act, float(eps)
+        return la_group_norm(x, weight, bias, gate, act, ctx.eps)
+
+    @staticmethod
+    def backward(ctx, dy):
+        x, weight, bias, gate = ctx.saved_tensors
+        dx, dweight, dbias, dgate = la_group_norm_backward(x, weight, dy.contiguous(), bias, gate,
+                                                           ctx.act, ctx.eps)
+        return dx, dweight, dbias, dgate, None, None

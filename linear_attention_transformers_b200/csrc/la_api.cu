@@ -1994,3 +1994,5 @@ la_status la_get_device_error(la_stream_t stream) {
 }
 
 }  // extern "C"
+
+#include "la_gated_api.cuh"

@@ -1,0 +1,424 @@
+// la_gated_api.cuh — entry points of gated linear attention and the head-row
+// group norm (declared in include/la_api.h): argument checks, workspace plans
+// and launches.  Included by la_api.cu, whose checks and helpers it uses.
+#pragma once
+
+#include "la_gated_decode.cuh"
+#include "la_gated_generic.cuh"
+#include "la_norm.cuh"
+
+namespace {
+
+constexpr int64_t kMaxBlocks = (int64_t(1) << 31) - 1;
+
+// ------------------------------------------------------------------ the plan
+// Records of D*D float32 per key/value head and 64-token chunk: the state
+// entering each chunk (S), and for the backward the gradient of the state
+// leaving it (R), each with its chunks' gate products.  A head of one chunk
+// with neither state given needs none.
+struct GatedPlan {
+    int64_t nchunk = 0;
+    size_t rec_bytes = 0, tot_bytes = 0;
+    size_t s_rec = 0, s_tot = 0, r_rec = 0, r_tot = 0, bytes = 0;
+};
+
+GatedPlan plan_gated(la_op op, int64_t B, int64_t Hkv, int64_t N, int64_t D) {
+    GatedPlan p;
+    const int64_t kvh = B * Hkv;
+    p.nchunk = (N + la::kGatedC - 1) / la::kGatedC;
+    p.rec_bytes = round_up(size_t(kvh) * size_t(p.nchunk) * size_t(D * D) * 4, 256);
+    p.tot_bytes = round_up(size_t(kvh) * size_t(p.nchunk) * 4, 256);
+    p.s_rec = 0;
+    p.s_tot = p.rec_bytes;
+    p.bytes = p.rec_bytes + p.tot_bytes;
+    if (op == LA_OP_BACKWARD) {
+        p.r_rec = p.bytes;
+        p.r_tot = p.r_rec + p.rec_bytes;
+        p.bytes += p.rec_bytes + p.tot_bytes;
+    }
+    return p;
+}
+
+// Sizes a gated launch can take: one block per 64 tokens of a head.
+la_status check_gated(int64_t B, int64_t H, int64_t Hkv, int64_t N, int64_t D, la_dtype dt) {
+    la_status s;
+    if (dt != LA_F32 && dt != LA_BF16) return LA_ERR_INVALID_ARG;
+    if ((s = check_sizes(B, H, N, D)) != LA_OK) return s;
+    if ((s = check_group(H, Hkv)) != LA_OK) return s;
+    if (N > 0 && B * H > kMaxBlocks / ((N + la::kGatedC - 1) / la::kGatedC))
+        return LA_ERR_UNSUPPORTED;
+    return LA_OK;
+}
+
+// Gates are read and written one by one, so a slice of a larger tensor will do.
+la_status check_gate_ptr(const void* p, la_dtype dt) {
+    const uintptr_t mask = dt == LA_F32 ? 3u : 1u;
+    return p == nullptr || (reinterpret_cast<uintptr_t>(p) & mask) ? LA_ERR_INVALID_ARG : LA_OK;
+}
+
+la_status check_opt(const void* p) {
+    return p != nullptr && !aligned16(p) ? LA_ERR_INVALID_ARG : LA_OK;
+}
+
+template <typename K>
+la_status allow_smem(K kern, size_t bytes) {
+    if (cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             int(bytes)))
+        return cuda_fail("cudaFuncSetAttribute", e);
+    return LA_OK;
+}
+
+// ------------------------------------------------------ the plain-core kernels
+// Border states of every chunk: parts, then the recurrence.  `last` (may be
+// null) receives the state after the last chunk walked.
+template <typename T, int D, bool REV>
+la_status gated_states(const T* A, const T* Bm, const T* lg, float* rec, float* tot,
+                       const float* first, float* last, int64_t kvh, int64_t N, int64_t nchunk,
+                       int group, float mul, cudaStream_t st) {
+    la_status s;
+    const int run = int(last ? nchunk : nchunk - 1);
+    if (run > 0) {
+        const size_t smem = size_t(2) * la::kGatedC * la::GatedTile::ld(D) * 4;
+        auto kern = la::gated_part_kernel<T, D, REV>;
+        if ((s = allow_smem(kern, smem)) != LA_OK) return s;
+        la::LaunchScope scope(REV ? "gated_part_rev" : "gated_part", st);
+        kern<<<unsigned(kvh * run), la::kGatedThreads, smem, st>>>(
+            A, Bm, lg, rec, tot, N, int(nchunk), run, REV && !last ? 1 : 0, group, mul);
+    }
+    const int per = D * D / 4;
+    const int64_t total = kvh * per;
+    la::LaunchScope scope(REV ? "gated_carry_rev" : "gated_carry", st);
+    la::gated_carry_kernel<REV><<<unsigned((total + 127) / 128), 128, 0, st>>>(
+        reinterpret_cast<float4*>(rec), tot, reinterpret_cast<const float4*>(first),
+        reinterpret_cast<float4*>(last), total, per, int(nchunk));
+    return launch_status();
+}
+
+template <typename T, int D, bool REV, bool TRANS>
+la_status gated_rows(const char* name, const T* R, const T* K, const T* V, const T* lg,
+                     const float* rec, T* out, int64_t heads, int64_t N, int64_t nchunk,
+                     int group, float in_mul, float st_mul, cudaStream_t st) {
+    la_status s;
+    const size_t smem = (size_t(3) * la::kGatedC * la::GatedTile::ld(D) +
+                         la::kGatedC * la::GatedTile::ld(la::kGatedC)) * 4;
+    auto kern = la::gated_rows_kernel<T, D, REV, TRANS>;
+    if ((s = allow_smem(kern, smem)) != LA_OK) return s;
+    la::LaunchScope scope(name, st);
+    kern<<<unsigned(heads * nchunk), la::kGatedThreads, smem, st>>>(
+        R, K, V, lg, rec, out, N, int(nchunk), group, in_mul, st_mul);
+    return launch_status();
+}
+
+template <typename T, int D>
+la_status run_gated_fwd(const void* q, const void* k, const void* v, const void* lg, void* o,
+                        const float* S_in, float* S_out, float scale, int64_t B, int64_t H,
+                        int64_t Hkv, int64_t N, char* ws, cudaStream_t st) {
+    const GatedPlan p = plan_gated(LA_OP_FORWARD, B, Hkv, N, D);
+    const int group = int(H / Hkv);
+    const T *tq = static_cast<const T*>(q), *tk = static_cast<const T*>(k),
+            *tv = static_cast<const T*>(v), *tl = static_cast<const T*>(lg);
+    float* rec = reinterpret_cast<float*>(ws + p.s_rec);
+    const bool through = p.nchunk > 1 || S_in || S_out;
+    if (through) {
+        la_status s = gated_states<T, D, false>(tk, tv, tl, rec,
+                                                reinterpret_cast<float*>(ws + p.s_tot), S_in,
+                                                S_out, B * Hkv, N, p.nchunk, 1, 1.f, st);
+        if (s != LA_OK) return s;
+    }
+    return gated_rows<T, D, false, false>("gated_o", tq, tk, tv, tl, through ? rec : nullptr,
+                                          static_cast<T*>(o), B * H, N, p.nchunk, group, scale,
+                                          scale, st);
+}
+
+template <typename T, int D>
+la_status run_gated_bwd(const void* q, const void* k, const void* v, const void* lg,
+                        const void* dO, const float* S_in, const float* dS_out, void* dq,
+                        void* dk, void* dv, void* dlg, float* dS_in, float scale, int64_t B,
+                        int64_t H, int64_t Hkv, int64_t N, char* ws, cudaStream_t st) {
+    la_status s;
+    const GatedPlan p = plan_gated(LA_OP_BACKWARD, B, Hkv, N, D);
+    const int group = int(H / Hkv);
+    const int64_t kvh = B * Hkv;
+    const T *tq = static_cast<const T*>(q), *tk = static_cast<const T*>(k),
+            *tv = static_cast<const T*>(v), *tl = static_cast<const T*>(lg),
+            *td = static_cast<const T*>(dO);
+    float *S = nullptr, *R = nullptr;
+    if (p.nchunk > 1 || S_in) {
+        S = reinterpret_cast<float*>(ws + p.s_rec);
+        if ((s = gated_states<T, D, false>(tk, tv, tl, S, reinterpret_cast<float*>(ws + p.s_tot),
+                                           S_in, nullptr, kvh, N, p.nchunk, 1, 1.f, st)) != LA_OK)
+            return s;
+    }
+    if (p.nchunk > 1 || dS_out || dS_in) {
+        R = reinterpret_cast<float*>(ws + p.r_rec);
+        if ((s = gated_states<T, D, true>(tq, td, tl, R, reinterpret_cast<float*>(ws + p.r_tot),
+                                          dS_out, dS_in, kvh, N, p.nchunk, group, scale, st)) !=
+            LA_OK)
+            return s;
+    }
+    if ((s = gated_rows<T, D, false, true>("gated_dq", td, tv, tk, tl, S, static_cast<T*>(dq),
+                                           B * H, N, p.nchunk, group, scale, scale, st)) != LA_OK)
+        return s;
+    if ((s = gated_rows<T, D, true, true>("gated_dk", tv, td, tq, tl, R, static_cast<T*>(dk), kvh,
+                                          N, p.nchunk, group, scale, 1.f, st)) != LA_OK)
+        return s;
+    if ((s = gated_rows<T, D, true, false>("gated_dv", tk, tq, td, tl, R, static_cast<T*>(dv),
+                                           kvh, N, p.nchunk, group, scale, 1.f, st)) != LA_OK)
+        return s;
+    const size_t smem = size_t(4) * la::kGatedC * la::GatedTile::ld(D) * 4;
+    auto kern = la::gated_dgate_kernel<T, D>;
+    if ((s = allow_smem(kern, smem)) != LA_OK) return s;
+    la::LaunchScope scope("gated_dgate", st);
+    kern<<<unsigned(kvh * p.nchunk), la::kGatedThreads, smem, st>>>(
+        tq, tk, tv, td, tl, S, R, static_cast<T*>(dlg), N, int(p.nchunk), group, scale);
+    return launch_status();
+}
+
+// fn.template operator()<T, D>() for the call's type and head size
+template <typename Fn>
+la_status with_type_and_size(la_dtype dt, int64_t D, Fn&& fn) {
+    auto size = [&](auto t) {
+        using T = decltype(t);
+        switch (D) {
+            case 16: return fn(t, std::integral_constant<int, 16>{});
+            case 32: return fn(t, std::integral_constant<int, 32>{});
+            case 64: return fn(t, std::integral_constant<int, 64>{});
+            default: return fn(T{}, std::integral_constant<int, 128>{});
+        }
+    };
+    return dt == LA_F32 ? size(float{}) : size(__nv_bfloat16{});
+}
+
+template <typename T, int D>
+la_status run_gated_step(float* S, const void* q, const void* k, const void* v, const void* lg,
+                         void* o, float scale, int64_t kvh, int G, cudaStream_t st) {
+    const T *tq = static_cast<const T*>(q), *tk = static_cast<const T*>(k),
+            *tv = static_cast<const T*>(v), *tl = static_cast<const T*>(lg);
+    la::LaunchScope scope("gated_step", st);
+    constexpr int DC = D / 4 < 16 ? 16 : D / 4;
+    if (kvh < 4 * num_sms())
+        la::gated_step_kernel<T, D, DC><<<unsigned(kvh * (D / DC)), 2 * D, 0, st>>>(
+            S, tq, tk, tv, tl, static_cast<T*>(o), G, scale);
+    else
+        la::gated_step_kernel<T, D, D><<<unsigned(kvh), 2 * D, 0, st>>>(
+            S, tq, tk, tv, tl, static_cast<T*>(o), G, scale);
+    return launch_status();
+}
+
+// ------------------------------------------------------------------ group norm
+struct NormPlan {
+    int groups = 0, span = 0, slots = 0, threads = 0, spans = 0, blocks = 0;
+    size_t bytes = 0;  // backward: partial sums
+};
+
+// A block covers 256 groups of 16 bytes of a token's channels, or several
+// tokens of fewer.  The tokens are dealt over as many blocks as keep every SM
+// full (8 blocks of 256 threads; 2 for the backward, whose registers hold the
+// channel sums and whose partial rows are read again), each block at least one.
+NormPlan plan_norm(int64_t B, int64_t H, int64_t N, int64_t D, la_dtype dt, bool bwd) {
+    NormPlan p;
+    p.groups = int(H * D * (dt == LA_F32 ? 4 : 2) / 16);
+    p.span = std::min(p.groups, 256);
+    p.slots = std::max(1, 256 / p.span);
+    p.threads = (p.span * p.slots + 31) / 32 * 32;
+    p.spans = (p.groups + p.span - 1) / p.span;
+    const int64_t tokens = B * N;
+    const int64_t want = std::max<int64_t>(1, int64_t(num_sms()) * (bwd ? 2 : 8) / p.spans);
+    p.blocks = int(std::max<int64_t>(1, std::min(want, (tokens + p.slots - 1) / p.slots)));
+    if (bwd) p.bytes = size_t(2) * size_t(p.blocks) * size_t(H * D) * 4;
+    return p;
+}
+
+la_status check_norm(int64_t B, int64_t H, int64_t N, int64_t D, la_dtype dt, la_act act,
+                     float eps) {
+    if (dt != LA_F32 && dt != LA_BF16) return LA_ERR_INVALID_ARG;
+    if (act != LA_ACT_IDENTITY && act != LA_ACT_SILU) return LA_ERR_INVALID_ARG;
+    if (!(eps > 0.f) || eps > 3.0e38f) return LA_ERR_INVALID_ARG;  // NaN fails too
+    la_status s = check_sizes(B, H, N, D);
+    if (s != LA_OK) return s;
+    return H * D > (int64_t(1) << 24) ? LA_ERR_UNSUPPORTED : LA_OK;
+}
+
+template <typename T, int D, bool BWD>
+la_status launch_norm(const la::NormParams& prm, const NormPlan& p, bool gate, la_act act,
+                      cudaStream_t st) {
+    const dim3 grid(unsigned(p.blocks), unsigned(p.spans));
+    auto go = [&](auto G, auto A) {
+        la::LaunchScope scope(BWD ? "group_norm_bwd" : "group_norm", st);
+        la::group_norm_kernel<T, D, BWD, decltype(G)::value, decltype(A)::value>
+            <<<grid, unsigned(p.threads), 0, st>>>(prm);
+        return launch_status();
+    };
+    using std::integral_constant;
+    if (gate)
+        return act == LA_ACT_SILU ? go(std::true_type{}, integral_constant<int, la::ACT_SILU>{})
+                                  : go(std::true_type{}, integral_constant<int, la::ACT_IDENTITY>{});
+    return act == LA_ACT_SILU ? go(std::false_type{}, integral_constant<int, la::ACT_SILU>{})
+                              : go(std::false_type{}, integral_constant<int, la::ACT_IDENTITY>{});
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t la_workspace_size_gated(la_op op, int64_t B, int64_t H, int64_t Hkv, int64_t N, int64_t D,
+                               la_dtype dt) {
+    if (op != LA_OP_FORWARD && op != LA_OP_BACKWARD) return 0;
+    if (check_gated(B, H, Hkv, N, D, dt) != LA_OK || B == 0 || H == 0 || N == 0) return 0;
+    return plan_gated(op, B, Hkv, N, D).bytes;
+}
+
+la_status la_forward_gated(const void* q, const void* k, const void* v, const void* log_gate,
+                           void* o, const float* S_in, float* S_out, float scale, int64_t B,
+                           int64_t H, int64_t Hkv, int64_t N, int64_t D, la_dtype dt,
+                           void* workspace, size_t workspace_bytes, la_stream_t stream) {
+    la_status s;
+    if ((s = check_gated(B, H, Hkv, N, D, dt)) != LA_OK) return s;
+    if ((s = check_opt(S_in)) != LA_OK || (s = check_opt(S_out)) != LA_OK) return s;
+    if (S_in && S_in == S_out) return LA_ERR_INVALID_ARG;
+    if ((s = check_opt(workspace)) != LA_OK) return s;
+    if (B == 0 || H == 0) return LA_OK;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    const size_t state = size_t(B) * size_t(Hkv) * size_t(D * D) * 4;
+    if (N == 0) {  // the state passes through
+        if (!S_out) return LA_OK;
+        const cudaError_t e = S_in ? cudaMemcpyAsync(S_out, S_in, state,
+                                                     cudaMemcpyDeviceToDevice, st)
+                                   : cudaMemsetAsync(S_out, 0, state, st);
+        return e == cudaSuccess ? LA_OK : cuda_fail("la_forward_gated: state copy", e);
+    }
+    if ((s = check_ptr(q)) || (s = check_ptr(k)) || (s = check_ptr(v)) ||
+        (s = check_gate_ptr(log_gate, dt)) || (s = check_ptr(o)))
+        return s;
+    if (workspace == nullptr ||
+        workspace_bytes < la_workspace_size_gated(LA_OP_FORWARD, B, H, Hkv, N, D, dt))
+        return LA_ERR_WORKSPACE;
+    if ((s = bind_context()) != LA_OK) return s;
+    char* ws = static_cast<char*>(workspace);
+    return with_type_and_size(dt, D, [&](auto t, auto d) {
+        return run_gated_fwd<decltype(t), decltype(d)::value>(q, k, v, log_gate, o, S_in, S_out,
+                                                              scale, B, H, Hkv, N, ws, st);
+    });
+}
+
+la_status la_backward_gated(const void* q, const void* k, const void* v, const void* log_gate,
+                            const void* dO, const float* S_in, const float* dS_out, void* dq,
+                            void* dk, void* dv, void* dlog_gate, float* dS_in, float scale,
+                            int64_t B, int64_t H, int64_t Hkv, int64_t N, int64_t D, la_dtype dt,
+                            void* workspace, size_t workspace_bytes, la_stream_t stream) {
+    la_status s;
+    if ((s = check_gated(B, H, Hkv, N, D, dt)) != LA_OK) return s;
+    if ((s = check_opt(S_in)) != LA_OK || (s = check_opt(dS_out)) != LA_OK ||
+        (s = check_opt(dS_in)) != LA_OK)
+        return s;
+    if (dS_in && (dS_in == dS_out || dS_in == S_in)) return LA_ERR_INVALID_ARG;
+    if ((s = check_opt(workspace)) != LA_OK) return s;
+    if (B == 0 || H == 0) return LA_OK;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    const size_t state = size_t(B) * size_t(Hkv) * size_t(D * D) * 4;
+    if (N == 0) {  // the state's gradient passes through
+        if (!dS_in) return LA_OK;
+        const cudaError_t e = dS_out ? cudaMemcpyAsync(dS_in, dS_out, state,
+                                                       cudaMemcpyDeviceToDevice, st)
+                                     : cudaMemsetAsync(dS_in, 0, state, st);
+        return e == cudaSuccess ? LA_OK : cuda_fail("la_backward_gated: state copy", e);
+    }
+    if ((s = check_ptr(q)) || (s = check_ptr(k)) || (s = check_ptr(v)) ||
+        (s = check_gate_ptr(log_gate, dt)) || (s = check_ptr(dO)) || (s = check_ptr(dq)) ||
+        (s = check_ptr(dk)) || (s = check_ptr(dv)) || (s = check_gate_ptr(dlog_gate, dt)))
+        return s;
+    if (workspace == nullptr ||
+        workspace_bytes < la_workspace_size_gated(LA_OP_BACKWARD, B, H, Hkv, N, D, dt))
+        return LA_ERR_WORKSPACE;
+    if ((s = bind_context()) != LA_OK) return s;
+    char* ws = static_cast<char*>(workspace);
+    return with_type_and_size(dt, D, [&](auto t, auto d) {
+        return run_gated_bwd<decltype(t), decltype(d)::value>(
+            q, k, v, log_gate, dO, S_in, dS_out, dq, dk, dv, dlog_gate, dS_in, scale, B, H, Hkv,
+            N, ws, st);
+    });
+}
+
+la_status la_decode_step_gated(float* S, const void* q, const void* k, const void* v,
+                               const void* log_gate, void* o, float scale, int64_t B, int64_t H,
+                               int64_t Hkv, int64_t D, la_dtype dt, la_stream_t stream) {
+    la_status s;
+    if ((s = check_gated(B, H, Hkv, 1, D, dt)) != LA_OK) return s;
+    if (B == 0 || H == 0) return LA_OK;
+    if (B * Hkv > kMaxBlocks / 8) return LA_ERR_UNSUPPORTED;
+    if ((s = check_ptr(S)) || (s = check_ptr(q)) || (s = check_ptr(k)) || (s = check_ptr(v)) ||
+        (s = check_gate_ptr(log_gate, dt)) || (s = check_ptr(o)))
+        return s;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    return with_type_and_size(dt, D, [&](auto t, auto d) {
+        return run_gated_step<decltype(t), decltype(d)::value>(S, q, k, v, log_gate, o, scale,
+                                                               B * Hkv, int(H / Hkv), st);
+    });
+}
+
+la_status la_group_norm(const void* x, const void* gate, const float* weight, const float* bias,
+                        void* y, float eps, la_act act, int64_t B, int64_t H, int64_t N,
+                        int64_t D, la_dtype dt, la_stream_t stream) {
+    la_status s;
+    if ((s = check_norm(B, H, N, D, dt, act, eps)) != LA_OK) return s;
+    if ((s = check_opt(gate)) != LA_OK || (s = check_opt(bias)) != LA_OK) return s;
+    if (B == 0 || H == 0 || N == 0) return LA_OK;
+    if ((s = check_ptr(x)) || (s = check_ptr(weight)) || (s = check_ptr(y))) return s;
+    const NormPlan p = plan_norm(B, H, N, D, dt, false);
+    la::NormParams prm{};
+    prm.x = x, prm.gate = gate, prm.weight = weight, prm.bias = bias, prm.y = y;
+    prm.tokens = B * N, prm.N = N, prm.H = int(H), prm.groups = p.groups;
+    prm.span = p.span, prm.slots = p.slots, prm.eps = eps;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    return with_type_and_size(dt, D, [&](auto t, auto d) {
+        return launch_norm<decltype(t), decltype(d)::value, false>(prm, p, gate != nullptr, act,
+                                                                   st);
+    });
+}
+
+size_t la_workspace_size_group_norm(int64_t B, int64_t H, int64_t N, int64_t D, la_dtype dt) {
+    if (check_norm(B, H, N, D, dt, LA_ACT_IDENTITY, 1.f) != LA_OK) return 0;
+    if (B == 0 || H == 0 || N == 0) return 0;
+    return plan_norm(B, H, N, D, dt, true).bytes;
+}
+
+la_status la_group_norm_backward(const void* x, const void* gate, const float* weight,
+                                 const float* bias, const void* dy, void* dx, void* dgate,
+                                 float* dweight, float* dbias, float eps, la_act act, int64_t B,
+                                 int64_t H, int64_t N, int64_t D, la_dtype dt, void* workspace,
+                                 size_t workspace_bytes, la_stream_t stream) {
+    la_status s;
+    if ((s = check_norm(B, H, N, D, dt, act, eps)) != LA_OK) return s;
+    if ((s = check_opt(gate)) || (s = check_opt(bias)) || (s = check_opt(dgate)) ||
+        (s = check_opt(dbias)) || (s = check_opt(workspace)))
+        return s;
+    if ((gate == nullptr) != (dgate == nullptr)) return LA_ERR_INVALID_ARG;
+    if (B == 0 || H == 0) return LA_OK;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if ((s = check_ptr(weight)) || (s = check_ptr(dweight))) return s;
+    if (N == 0) {  // no rows: the channel sums are empty
+        cudaError_t e = cudaMemsetAsync(dweight, 0, size_t(H * D) * 4, st);
+        if (e == cudaSuccess && dbias) e = cudaMemsetAsync(dbias, 0, size_t(H * D) * 4, st);
+        return e == cudaSuccess ? LA_OK : cuda_fail("la_group_norm_backward: zeros", e);
+    }
+    if ((s = check_ptr(x)) || (s = check_ptr(dy)) || (s = check_ptr(dx))) return s;
+    const NormPlan p = plan_norm(B, H, N, D, dt, true);
+    if (workspace == nullptr || workspace_bytes < p.bytes) return LA_ERR_WORKSPACE;
+    la::NormParams prm{};
+    prm.x = x, prm.gate = gate, prm.dy = dy, prm.weight = weight, prm.bias = bias;
+    prm.dx = dx, prm.dgate = dgate, prm.part = static_cast<float*>(workspace);
+    prm.tokens = B * N, prm.N = N, prm.H = int(H), prm.groups = p.groups;
+    prm.span = p.span, prm.slots = p.slots, prm.eps = eps;
+    s = with_type_and_size(dt, D, [&](auto t, auto d) {
+        return launch_norm<decltype(t), decltype(d)::value, true>(prm, p, gate != nullptr, act,
+                                                                  st);
+    });
+    if (s != LA_OK) return s;
+    const int C = int(H * D);
+    la::LaunchScope scope("norm_sum", st);
+    la::norm_sum_kernel<<<dim3(unsigned((C + 31) / 32), 2), 512, 0, st>>>(prm.part, dweight, dbias,
+                                                                         p.blocks, C);
+    return launch_status();
+}
+
+}  // extern "C"

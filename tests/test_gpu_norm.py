@@ -1,0 +1,115 @@
+"""The head-row group norm on the GPU against the float64 oracle."""
+import pytest
+import torch
+
+from gated_util import MAX, REL, close
+from linear_attention_transformers_b200 import api
+from oracle import gated
+
+pytestmark = pytest.mark.gpu
+
+TYPES = [torch.float32, torch.bfloat16]
+# B, H, N: fewer channels than a block, a block, several blocks; odd counts
+SHAPES = [(1, 1, 1), (7, 16, 1), (1, 3, 5), (2, 6, 129), (3, 5, 333), (1, 40, 17), (2, 32, 1000), (1, 1, 4099)]
+
+
+def tensors(B, H, N, D, dtype, seed):
+    g = torch.Generator().manual_seed(seed)
+    rows = torch.exp(torch.randn(B, H, N, 1, generator=g))
+    x = ((torch.randn(B, H, N, D, generator=g) + 0.3) * rows).to(dtype).cuda()
+    w = (1 + 0.2 * torch.randn(H * D, generator=g)).cuda()
+    b = (0.2 * torch.randn(H * D, generator=g)).cuda()
+    gate, dy = torch.randn(2, B, N, H * D, generator=g).to(dtype).cuda().unbind(0)
+    return x, w, b, gate.contiguous(), dy.contiguous()
+
+
+@pytest.mark.parametrize("shape", SHAPES)
+@pytest.mark.parametrize("D", [16, 32, 64, 128])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_forward_and_backward(dtype, D, shape):
+    x, w, b, gate, dy = tensors(*shape, D, dtype, D)
+    for bias, gt, act in ((b, gate, "silu"), (None, gate, "identity"), (b, None, "silu"),
+                          (None, None, "identity")):
+        y = api.la_group_norm(x, w, bias, gt, act, 1e-4)
+        close(y, gated.group_norm(x, w, bias, gt, act, 1e-4), REL[dtype], MAX[dtype], "y")
+        got = api.la_group_norm_backward(x, w, dy, bias, gt, act, 1e-4)
+        ref = gated.group_norm_backward(x, w, dy, bias, gt, act, 1e-4)
+        for n, g, r in zip(("dx", "dweight", "dbias", "dgate"), got, ref):
+            if g is None:
+                assert (n == "dbias" and bias is None) or (n == "dgate" and gt is None)
+                continue
+            # channel sums: float32 terms (each within 2^-20), added over at most
+            # 4099 tokens with errors that add like a random walk
+            rel, most = (2.0 ** -18, 2.0 ** -16) if n in ("dweight", "dbias") else (REL[dtype], MAX[dtype])
+            close(g, r, rel, most, n)
+        again = api.la_group_norm_backward(x, w, dy, bias, gt, act, 1e-4)
+        for a, c in zip(got, again):
+            assert (a is None and c is None) or torch.equal(a, c)
+
+
+def test_rows_of_one_value_and_of_zeros():
+    # no variance: x_hat is zero (or what rounding leaves over sqrt(eps)), never NaN
+    x, w, b, gate, dy = tensors(1, 2, 6, 64, torch.float32, 3)
+    x[0, 0, 1] = 0
+    x[0, 1, 2] = 5.0
+    y = api.la_group_norm(x, w, b, gate)
+    close(y, gated.group_norm(x, w, b, gate), REL[torch.float32], MAX[torch.float32], "y")
+    got = api.la_group_norm_backward(x, w, dy, b, gate)
+    ref = gated.group_norm_backward(x, w, dy, b, gate)
+    for g, r in zip(got, ref):
+        close(g, r, REL[torch.float32], MAX[torch.float32], "gradient")
+
+
+def test_a_row_that_is_not_finite_stays_alone():
+    x, w, b, gate, _ = tensors(1, 3, 9, 32, torch.float32, 4)
+    y = api.la_group_norm(x, w, b, gate)
+    x2 = x.clone()
+    x2[0, 1, 4, 7] = float("nan")
+    x2[0, 2, 5, 0] = float("inf")
+    y2 = api.la_group_norm(x2, w, b, gate)
+    keep = torch.ones(1, 9, 96, dtype=torch.bool, device="cuda")
+    keep[0, 4, 32:64] = False
+    keep[0, 5, 64:96] = False
+    assert torch.equal(y[keep], y2[keep]) and not torch.isfinite(y2[~keep]).any()
+
+
+def test_no_rows():
+    x = torch.empty(2, 3, 0, 64, device="cuda")
+    w = torch.ones(192, device="cuda")
+    e = torch.empty(2, 0, 192, device="cuda")
+    assert api.la_group_norm(x, w).shape == (2, 0, 192)
+    dx, dw, db, dg = api.la_group_norm_backward(x, w, e, bias=w, gate=e)
+    assert dx.shape == x.shape and dg.shape == e.shape and not dw.any() and not db.any()
+
+
+def test_long_offsets():
+    # more than 2^31 elements: the last rows equal a call on them alone
+    H, N, D = 64, (1 << 31) // (64 * 128) + 5, 128
+    x = torch.randn(1, H, N, D, device="cuda", dtype=torch.bfloat16)
+    w = torch.ones(H * D, device="cuda")
+    y = api.la_group_norm(x, w)
+    y2 = api.la_group_norm(x[:, :, -7:].contiguous(), w)
+    assert torch.equal(y[:, -7:], y2)
+
+
+def test_streams_and_refusals():
+    x, w, b, gate, dy = tensors(2, 4, 50, 64, torch.bfloat16, 9)
+    want = api.la_group_norm(x, w, b, gate)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    got = api.la_group_norm(x, w, b, gate, stream=s)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+    for kw in (dict(eps=0.0), dict(eps=float("nan")), dict(eps=-1.0), dict(eps=float("inf"))):
+        with pytest.raises(api.LinearAttentionError):
+            api.la_group_norm(x, w, b, gate, **kw)
+    for args in ((x, w.bfloat16()), (x, w[:-1]), (x[0], w), (x.transpose(1, 2), w), (x, w, b, gate.float()),
+                 (x, w, b, gate.transpose(0, 1)), (x, w, b[:-1])):
+        with pytest.raises(ValueError):
+            api.la_group_norm(*args)
+    with pytest.raises(ValueError):
+        api.la_group_norm(x, w, act="gelu")
+    with pytest.raises(ValueError):
+        api.la_group_norm_backward(x, w, dy, dbias=torch.empty_like(w))
+    with pytest.raises(ValueError):
+        api.la_group_norm_backward(x, w, dy.float())
