@@ -5,6 +5,7 @@
 
 #include "la_gated_decode.cuh"
 #include "la_gated_generic.cuh"
+#include "la_gated_tc.cuh"
 #include "la_norm.cuh"
 
 namespace {
@@ -38,6 +39,50 @@ GatedPlan plan_gated(la_op op, int64_t B, int64_t Hkv, int64_t N, int64_t D) {
     }
     return p;
 }
+
+// Tensor-core path (bf16, D = 64 or 128): 128-token blocks, spans of nb
+// blocks.  One float32 record array serves both directions' parts in turn; the
+// states entering the spans are bf16, one array each for S and R.
+struct GatedTcPlan {
+    int64_t nblk = 0;
+    int nb = 0, nspan = 0;
+    size_t rec = 0, tot = 0, s_enter = 0, r_enter = 0, qrow = 0, krow = 0, colv = 0, bytes = 0;
+};
+
+GatedTcPlan plan_gated_tc(la_op op, int64_t B, int64_t H, int64_t Hkv, int64_t N, int64_t D) {
+    GatedTcPlan p;
+    p.nblk = (N + la::kGtC - 1) / la::kGtC;
+    // A sequence of one span needs no border states, so up to four blocks are
+    // one.  Longer spans move fewer state bytes (D^2 a span) and take more C x C
+    // products (nb + 1 over 2 a block): D = 128 gains from two blocks (131072
+    // tokens, 32 heads, forward: 2161 us with one, 1952 with two, 2083 with
+    // four), D = 64, whose states are a quarter, does not (8192 tokens, 128
+    // heads, backward: 883, 1026, 1169 us).
+    p.nb = p.nblk <= 1 ? 1 : p.nblk == 2 ? 2 : p.nblk <= 4 ? 4 : D == 64 ? 1 : 2;
+    p.nspan = int((p.nblk + p.nb - 1) / p.nb);
+    size_t at = 0;
+    auto take = [&](size_t n) {
+        const size_t o = at;
+        at += round_up(n, 256);
+        return o;
+    };
+    const size_t states = size_t(B) * size_t(Hkv) * size_t(p.nspan) * size_t(D * D);
+    p.rec = take(states * 4);
+    p.tot = take(size_t(B) * size_t(Hkv) * size_t(p.nspan) * 4);
+    p.s_enter = take(states * 2);
+    if (op == LA_OP_BACKWARD) {
+        const size_t qt = size_t(B) * size_t(H) * size_t(N) * 4;
+        p.r_enter = take(states * 2);
+        p.qrow = take(2 * qt);
+        p.krow = take(size_t(B) * size_t(Hkv) * size_t(N) * 8);
+        p.colv = take(qt * size_t(4 * p.nb));
+    }
+    p.bytes = at;
+    return p;
+}
+
+template <typename T, int D>
+constexpr bool gated_on_tensor_cores = std::is_same<T, __nv_bfloat16>::value && (D == 64 || D == 128);
 
 // Sizes a gated launch can take: one block per 64 tokens of a head.
 la_status check_gated(int64_t B, int64_t H, int64_t Hkv, int64_t N, int64_t D, la_dtype dt) {
@@ -106,6 +151,145 @@ la_status gated_rows(const char* name, const T* R, const T* K, const T* V, const
     la::LaunchScope scope(name, st);
     kern<<<unsigned(heads * nchunk), la::kGatedThreads, smem, st>>>(
         R, K, V, lg, rec, out, N, int(nchunk), group, in_mul, st_mul);
+    return launch_status();
+}
+
+// ---------------------------------------------------- the tensor-core kernels
+template <int D, bool REV>
+la_status gated_tc_states(const void* A, const void* Bm, const void* lg, const GatedTcPlan& p,
+                          char* ws, size_t enter, const float* first, float* last, int64_t heads,
+                          int64_t kvh, int64_t N, int group, float mul, cudaStream_t st) {
+    la_status s;
+    const int run = last ? p.nspan : p.nspan - 1;
+    float* rec = reinterpret_cast<float*>(ws + p.rec);
+    float* tot = reinterpret_cast<float*>(ws + p.tot);
+    if (run > 0) {
+        using Cfg = la::GatedSpanCfg<D>;
+        la::GatedSpanParams prm;
+        memset(&prm, 0, sizeof(prm));
+        if (!make_qkv_map(&prm.tm_a, A, heads, N, D, la::kGtC) ||
+            !make_qkv_map(&prm.tm_b, Bm, heads, N, D, la::kGtC))
+            return LA_ERR_CUDA;
+        prm.lg = static_cast<const __nv_bfloat16*>(lg);
+        prm.rec = rec, prm.tot = tot, prm.N = N;
+        prm.items = kvh * run, prm.nspan = p.nspan, prm.spans_run = run;
+        prm.span0 = REV && !last ? 1 : 0;
+        prm.nb = p.nb, prm.nblk = int(p.nblk), prm.group = group, prm.mul = mul;
+        auto kern = la::gated_span_kernel<D, REV>;
+        if ((s = allow_smem(kern, Cfg::SMEM)) != LA_OK) return s;
+        const unsigned grid = unsigned(std::min<int64_t>(prm.items, int64_t(num_sms()) * Cfg::CTAS));
+        la::LaunchScope scope(REV ? "gated_span_rev" : "gated_span", st);
+        kern<<<grid, la::kGatedSpanThreads, Cfg::SMEM, st>>>(prm);
+        if ((s = launch_status()) != LA_OK) return s;
+    }
+    const int per = D * D / 4;
+    const int64_t total = kvh * per;
+    la::LaunchScope scope(REV ? "gated_border_rev" : "gated_border", st);
+    la::gated_border_kernel<REV><<<unsigned((total + 127) / 128), 128, 0, st>>>(
+        reinterpret_cast<const float4*>(rec), tot, reinterpret_cast<const float4*>(first),
+        reinterpret_cast<float4*>(last), reinterpret_cast<uint2*>(ws + enter), total, per,
+        p.nspan);
+    return launch_status();
+}
+
+// rows, columns, values, second rows (XTRA), states entering the spans (null:
+// none), output; `heads` row heads, `colh` column heads
+struct GatedBlockCall {
+    const char* name;
+    const void *row, *col, *val, *row2, *state;
+    void* out;
+    float *rowv, *colv;
+    int64_t heads, colh, kvh;
+    float in_mul, st_mul;
+};
+
+template <int D, bool REV, bool TRANS, int XTRA>
+la_status gated_tc_block(const GatedBlockCall& c, const void* lg, const GatedTcPlan& p, int64_t N,
+                         int group, cudaStream_t st) {
+    using Cfg = la::GatedBlockCfg<D, XTRA>;
+    la_status s;
+    la::GatedBlockParams prm;
+    memset(&prm, 0, sizeof(prm));
+    if (!make_qkv_map(&prm.tm_row, c.row, c.heads, N, D, la::kGtC) ||
+        !make_qkv_map(&prm.tm_col, c.col, c.colh, N, D, la::kGtC) ||
+        !make_qkv_map(&prm.tm_val, c.val, c.colh, N, D, la::kGtC) ||
+        !make_qkv_map(&prm.tm_out, c.out, c.heads, N, D, la::kGtC) ||
+        (XTRA && !make_qkv_map(&prm.tm_row2, c.row2, c.heads, N, D, la::kGtC)) ||
+        (c.state && !make_qkv_map(&prm.tm_st, c.state, c.kvh * p.nspan, D, D, D)))
+        return LA_ERR_CUDA;
+    prm.lg = static_cast<const __nv_bfloat16*>(lg);
+    prm.rowv = c.rowv, prm.colv = c.colv, prm.N = N;
+    prm.items = c.heads * p.nblk, prm.heads = c.heads;
+    prm.nblk = int(p.nblk), prm.nb = p.nb, prm.nspan = p.nspan, prm.group = group;
+    prm.has_state = c.state != nullptr, prm.in_mul = c.in_mul, prm.st_mul = c.st_mul;
+    auto kern = la::gated_block_kernel<D, REV, TRANS, XTRA>;
+    if ((s = allow_smem(kern, Cfg::SMEM)) != LA_OK) return s;
+    const unsigned grid = unsigned(std::min<int64_t>(prm.items, int64_t(num_sms()) * Cfg::CTAS));
+    la::LaunchScope scope(c.name, st);
+    kern<<<grid, la::kGatedBlockThreads, Cfg::SMEM, st>>>(prm);
+    return launch_status();
+}
+
+template <int D>
+la_status run_gated_fwd_tc(const void* q, const void* k, const void* v, const void* lg, void* o,
+                           const float* S_in, float* S_out, float scale, int64_t B, int64_t H,
+                           int64_t Hkv, int64_t N, char* ws, cudaStream_t st) {
+    const GatedTcPlan p = plan_gated_tc(LA_OP_FORWARD, B, H, Hkv, N, D);
+    const int64_t kvh = B * Hkv;
+    const bool through = p.nspan > 1 || S_in || S_out;
+    if (through) {
+        la_status s = gated_tc_states<D, false>(k, v, lg, p, ws, p.s_enter, S_in, S_out, kvh, kvh,
+                                                N, 1, 1.f, st);
+        if (s != LA_OK) return s;
+    }
+    const bool state = p.nspan > 1 || S_in;
+    const GatedBlockCall c{"gated_o", q, k, v, nullptr, state ? ws + p.s_enter : nullptr, o,
+                           nullptr, nullptr, B * H, kvh, kvh, scale, scale};
+    return gated_tc_block<D, false, false, 0>(c, lg, p, N, int(H / Hkv), st);
+}
+
+template <int D>
+la_status run_gated_bwd_tc(const void* q, const void* k, const void* v, const void* lg,
+                           const void* dO, const float* S_in, const float* dS_out, void* dq,
+                           void* dk, void* dv, void* dlg, float* dS_in, float scale, int64_t B,
+                           int64_t H, int64_t Hkv, int64_t N, char* ws, cudaStream_t st) {
+    la_status s;
+    const GatedTcPlan p = plan_gated_tc(LA_OP_BACKWARD, B, H, Hkv, N, D);
+    const int group = int(H / Hkv);
+    const int64_t kvh = B * Hkv, qh = B * H;
+    const void *S = nullptr, *R = nullptr;
+    if (p.nspan > 1 || S_in) {
+        S = ws + p.s_enter;
+        if ((s = gated_tc_states<D, false>(k, v, lg, p, ws, p.s_enter, S_in, nullptr, kvh, kvh, N,
+                                           1, 1.f, st)) != LA_OK)
+            return s;
+    }
+    if (p.nspan > 1 || dS_out || dS_in) {
+        if ((s = gated_tc_states<D, true>(q, dO, lg, p, ws, p.r_enter, dS_out, dS_in, qh, kvh, N,
+                                          group, scale, st)) != LA_OK)
+            return s;
+        if (p.nspan > 1 || dS_out) R = ws + p.r_enter;
+    }
+    float* qrow = reinterpret_cast<float*>(ws + p.qrow);
+    float* krow = reinterpret_cast<float*>(ws + p.krow);
+    float* colv = reinterpret_cast<float*>(ws + p.colv);
+    const GatedBlockCall cq{"gated_dq", dO, v, k, q, S, dq, qrow, colv, qh, kvh, kvh, scale, scale};
+    if ((s = gated_tc_block<D, false, true, 2>(cq, lg, p, N, group, st)) != LA_OK) return s;
+    const GatedBlockCall ck{"gated_dk", v, dO, q, k, R, dk, krow, nullptr, kvh, qh, kvh, scale, 1.f};
+    s = R ? gated_tc_block<D, true, true, 1>(ck, lg, p, N, group, st)
+          : gated_tc_block<D, true, true, 0>(ck, lg, p, N, group, st);
+    if (s != LA_OK) return s;
+    const GatedBlockCall cv{"gated_dv", k, q, dO, nullptr, R, dv, nullptr, nullptr, kvh, qh, kvh,
+                            scale, 1.f};
+    if ((s = gated_tc_block<D, true, false, 0>(cv, lg, p, N, group, st)) != LA_OK) return s;
+    la::GatedDgateParams g{};
+    g.qrow = qrow, g.colv = colv, g.krow = R ? krow : nullptr;
+    g.S = static_cast<const __nv_bfloat16*>(S), g.R = static_cast<const __nv_bfloat16*>(R);
+    g.lg = static_cast<const __nv_bfloat16*>(lg), g.dlg = static_cast<__nv_bfloat16*>(dlg);
+    g.N = N, g.qheads = qh, g.kvh = kvh;
+    g.nspan = p.nspan, g.nb = p.nb, g.nblk = int(p.nblk), g.group = group;
+    la::LaunchScope scope("gated_dgate_sum", st);
+    la::gated_dgate_sum_kernel<D><<<unsigned(kvh * p.nspan), 256, 0, st>>>(g);
     return launch_status();
 }
 
@@ -265,7 +449,8 @@ size_t la_workspace_size_gated(la_op op, int64_t B, int64_t H, int64_t Hkv, int6
                                la_dtype dt) {
     if (op != LA_OP_FORWARD && op != LA_OP_BACKWARD) return 0;
     if (check_gated(B, H, Hkv, N, D, dt) != LA_OK || B == 0 || H == 0 || N == 0) return 0;
-    return plan_gated(op, B, Hkv, N, D).bytes;
+    return fast_path(dt, D) ? plan_gated_tc(op, B, H, Hkv, N, D).bytes
+                            : plan_gated(op, B, Hkv, N, D).bytes;
 }
 
 la_status la_forward_gated(const void* q, const void* k, const void* v, const void* log_gate,
@@ -296,8 +481,14 @@ la_status la_forward_gated(const void* q, const void* k, const void* v, const vo
     if ((s = bind_context()) != LA_OK) return s;
     char* ws = static_cast<char*>(workspace);
     return with_type_and_size(dt, D, [&](auto t, auto d) {
-        return run_gated_fwd<decltype(t), decltype(d)::value>(q, k, v, log_gate, o, S_in, S_out,
-                                                              scale, B, H, Hkv, N, ws, st);
+        using T = decltype(t);
+        constexpr int kD = decltype(d)::value;
+        if constexpr (gated_on_tensor_cores<T, kD>)
+            return run_gated_fwd_tc<kD>(q, k, v, log_gate, o, S_in, S_out, scale, B, H, Hkv, N, ws,
+                                        st);
+        else
+            return run_gated_fwd<T, kD>(q, k, v, log_gate, o, S_in, S_out, scale, B, H, Hkv, N, ws,
+                                        st);
     });
 }
 
@@ -333,9 +524,14 @@ la_status la_backward_gated(const void* q, const void* k, const void* v, const v
     if ((s = bind_context()) != LA_OK) return s;
     char* ws = static_cast<char*>(workspace);
     return with_type_and_size(dt, D, [&](auto t, auto d) {
-        return run_gated_bwd<decltype(t), decltype(d)::value>(
-            q, k, v, log_gate, dO, S_in, dS_out, dq, dk, dv, dlog_gate, dS_in, scale, B, H, Hkv,
-            N, ws, st);
+        using T = decltype(t);
+        constexpr int kD = decltype(d)::value;
+        if constexpr (gated_on_tensor_cores<T, kD>)
+            return run_gated_bwd_tc<kD>(q, k, v, log_gate, dO, S_in, dS_out, dq, dk, dv, dlog_gate,
+                                        dS_in, scale, B, H, Hkv, N, ws, st);
+        else
+            return run_gated_bwd<T, kD>(q, k, v, log_gate, dO, S_in, dS_out, dq, dk, dv, dlog_gate,
+                                        dS_in, scale, B, H, Hkv, N, ws, st);
     });
 }
 

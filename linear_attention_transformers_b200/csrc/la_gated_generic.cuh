@@ -431,10 +431,15 @@ gated_dgate_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __
             if (tid + o < 32) s += a;
             if (tid >= o) t += b;
         }
-        const float before = t - (t0 + t1);
+        // shifted, not subtracted: a token's own term may be larger than the rest
+        // by more than float32 holds
+        float before = __shfl_up_sync(0xffffffffu, t, 1);
+        float behind = __shfl_down_sync(0xffffffffu, s, 1);
+        if (tid == 0) before = 0.f;
+        if (tid == 31) behind = 0.f;
         const int64_t n = n0 + 2 * tid;
         if (n < N) dlg[head * N + n] = from_f32<T>(s + before + all);
-        if (n + 1 < N) dlg[head * N + n + 1] = from_f32<T>(s - d0 + (before + t0) + all);
+        if (n + 1 < N) dlg[head * N + n + 1] = from_f32<T>(d1 + behind + (before + t0) + all);
     }
 }
 
