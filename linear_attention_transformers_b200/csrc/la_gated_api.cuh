@@ -397,8 +397,7 @@ struct NormPlan {
 
 // A block covers 256 groups of 16 bytes of a token's channels, or several
 // tokens of fewer.  The tokens are dealt over as many blocks as keep every SM
-// full (8 blocks of 256 threads; 2 for the backward, whose registers hold the
-// channel sums and whose partial rows are read again), each block at least one.
+// full (kNormBlocks), each block at least one.
 NormPlan plan_norm(int64_t B, int64_t H, int64_t N, int64_t D, la_dtype dt, bool bwd) {
     NormPlan p;
     p.groups = int(H * D * (dt == LA_F32 ? 4 : 2) / 16);
@@ -407,7 +406,10 @@ NormPlan plan_norm(int64_t B, int64_t H, int64_t N, int64_t D, la_dtype dt, bool
     p.threads = (p.span * p.slots + 31) / 32 * 32;
     p.spans = (p.groups + p.span - 1) / p.span;
     const int64_t tokens = B * N;
-    const int64_t want = std::max<int64_t>(1, int64_t(num_sms()) * (bwd ? 2 : 8) / p.spans);
+    const int per_sm = dt == LA_F32 ? (bwd ? la::kNormBlocks<float, true> : la::kNormBlocks<float, false>)
+                                    : (bwd ? la::kNormBlocks<__nv_bfloat16, true>
+                                           : la::kNormBlocks<__nv_bfloat16, false>);
+    const int64_t want = std::max<int64_t>(1, int64_t(num_sms()) * per_sm / p.spans);
     p.blocks = int(std::max<int64_t>(1, std::min(want, (tokens + p.slots - 1) / p.slots)));
     if (bwd) p.bytes = size_t(2) * size_t(p.blocks) * size_t(H * D) * 4;
     return p;
@@ -427,10 +429,12 @@ template <typename T, int D, bool BWD>
 la_status launch_norm(const la::NormParams& prm, const NormPlan& p, bool gate, la_act act,
                       cudaStream_t st) {
     const dim3 grid(unsigned(p.blocks), unsigned(p.spans));
+    const size_t smem = size_t(la::kNormStages) * size_t(1 + gate + BWD) * size_t(p.threads) * 16;
     auto go = [&](auto G, auto A) {
+        auto kern = la::group_norm_kernel<T, D, BWD, decltype(G)::value, decltype(A)::value>;
+        if (la_status s = allow_smem(kern, smem)) return s;
         la::LaunchScope scope(BWD ? "group_norm_bwd" : "group_norm", st);
-        la::group_norm_kernel<T, D, BWD, decltype(G)::value, decltype(A)::value>
-            <<<grid, unsigned(p.threads), 0, st>>>(prm);
+        kern<<<grid, unsigned(p.threads), smem, st>>>(prm);
         return launch_status();
     };
     using std::integral_constant;
