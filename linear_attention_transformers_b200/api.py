@@ -88,6 +88,8 @@ class LinearAttentionError(RuntimeError):
 def load_library(path: str | None = None):
     """Load liblinattn.so (built in-tree by ``build.py``); raises if absent."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -532,13 +534,15 @@ class _LaunchOn:
             if stream.device != t.device:
                 raise ValueError(f"stream is on {stream.device}, the tensors on {t.device}")
             self._ctx = torch.cuda.stream(stream)
-        elif t.device.index != torch.cuda.current_device():
+        elif t.get_device() != torch.cuda.current_device():
             self._ctx = torch.cuda.device(t.device)
 
     def __enter__(self):
         if self._ctx is not None:
             self._ctx.__enter__()
-        return torch.cuda.current_stream().cuda_stream
+        # the handle without a Stream object around it (3 us less of a call that
+        # may take 10)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
     def __exit__(self, *exc):
         if self._ctx is not None:
@@ -546,8 +550,35 @@ class _LaunchOn:
         return None
 
 
+def _check_gated(name, q, k, v, log_gate, dims):
+    """q [B, H, (N,) D], k and v [B, Hkv, (N,) D], log_gate [B, Hkv (, N)] of one
+    device and type; returns their sizes and the library's type code."""
+    dtype, device, qs, ks = q.dtype, q.device, q.shape, k.shape
+    if not q.is_cuda:
+        raise ValueError(f"{name}: tensors must be on a CUDA device")
+    code = DTYPE.get(dtype)
+    if code is None:
+        raise ValueError(f"{name}: dtype must be float32 or bfloat16, got {dtype}")
+    if len(qs) != dims or len(ks) != dims:
+        raise ValueError(f"{name}: q must be [B, H, {'N, ' if dims == 4 else ''}D], k and v the same "
+                         "with Hkv heads")
+    H, Hkv = qs[1], ks[1]
+    if (v.shape != ks or log_gate.shape != ks[:-1] or ks[0] != qs[0] or ks[2:] != qs[2:]
+            or (H % Hkv if Hkv else H)):
+        raise ValueError(f"{name}: k and v must be [B, Hkv, ...] and log_gate their shape without D, "
+                         "with Hkv dividing q's heads")
+    for t in (k, v, log_gate):
+        if t.dtype is not dtype or t.device != device:
+            raise ValueError(f"{name}: all tensors need the same device and dtype")
+        if not t.is_contiguous():
+            raise ValueError(f"{name}: tensors must be contiguous")
+    if not q.is_contiguous():
+        raise ValueError(f"{name}: tensors must be contiguous")
+    return qs[0], H, Hkv, qs[2] if dims == 4 else 1, qs[-1], code
+
+
 def _check_like(name, what, t, ref, shape, dtype=None):
-    if (t.dtype != (dtype or ref.dtype) or tuple(t.shape) != tuple(shape)
+    if (t.dtype != (dtype or ref.dtype) or t.shape != tuple(shape)
             or t.device != ref.device or not t.is_contiguous()):
         raise ValueError(f"{name}: {what} must be contiguous {dtype or ref.dtype} {tuple(shape)} "
                          f"on {ref.device}")
@@ -579,12 +610,7 @@ def la_forward_gated(q, k, v, log_gate, scale: float = 1.0, S_in=None, o=None,
     state after the last token, in ``S_out`` if given.
     """
     lib = load_library()
-    _check_qkv("la_forward_gated", q)
-    if q.dim() != 4:
-        raise ValueError("la_forward_gated: q must be [B, H, N, D], k and v [B, Hkv, N, D]")
-    Hkv = _check_kv("la_forward_gated", q, k, v)
-    B, H, N, D = q.shape
-    _check_like("la_forward_gated", "log_gate", log_gate, q, (B, Hkv, N))
+    B, H, Hkv, N, D, code = _check_gated("la_forward_gated", q, k, v, log_gate, 4)
     for what, t in (("S_in", S_in), ("S_out", S_out)):
         if t is not None:
             _check_like("la_forward_gated", what, t, q, (B, Hkv, D, D), torch.float32)
@@ -596,9 +622,9 @@ def la_forward_gated(q, k, v, log_gate, scale: float = 1.0, S_in=None, o=None,
         if S_out is None and return_state:
             S_out = torch.empty((B, Hkv, D, D), dtype=torch.float32, device=q.device)
         ws, ws_bytes = _scratch("la_forward_gated", lib.la_workspace_size_gated(
-            LA_OP_FORWARD, B, H, Hkv, N, D, DTYPE[q.dtype]), workspace, q.device)
-        st = lib.la_forward_gated(_ptr(q), _ptr(k), _ptr(v), _ptr(log_gate), _ptr(o), _ptr(S_in),
-                                  _ptr(S_out), scale, B, H, Hkv, N, D, DTYPE[q.dtype], _ptr(ws),
+            LA_OP_FORWARD, B, H, Hkv, N, D, code), workspace, q.device)
+        st = lib.la_forward_gated(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_gate.data_ptr(), o.data_ptr(), _ptr(S_in),
+                                  _ptr(S_out), scale, B, H, Hkv, N, D, code, _ptr(ws),
                                   ws_bytes, handle)
     _check("la_forward_gated", st)
     return (o, S_out) if return_state else o
@@ -611,12 +637,8 @@ def la_backward_gated(q, k, v, log_gate, dO, scale: float = 1.0, S_in=None, dS_o
     (o, S_out) = la_forward_gated(q, k, v, log_gate, scale, S_in), and with
     ``return_dstate`` also the gradient of S_in.  ``dS_out`` None: zero."""
     lib = load_library()
-    _check_qkv("la_backward_gated", q, dO)
-    if q.dim() != 4:
-        raise ValueError("la_backward_gated: q must be [B, H, N, D], k and v [B, Hkv, N, D]")
-    Hkv = _check_kv("la_backward_gated", q, k, v)
-    B, H, N, D = q.shape
-    _check_like("la_backward_gated", "log_gate", log_gate, q, (B, Hkv, N))
+    B, H, Hkv, N, D, code = _check_gated("la_backward_gated", q, k, v, log_gate, 4)
+    _check_like("la_backward_gated", "dO", dO, q, q.shape)
     for what, t in (("S_in", S_in), ("dS_out", dS_out), ("dS_in", dS_in)):
         if t is not None:
             _check_like("la_backward_gated", what, t, q, (B, Hkv, D, D), torch.float32)
@@ -632,11 +654,11 @@ def la_backward_gated(q, k, v, log_gate, dO, scale: float = 1.0, S_in=None, dS_o
         if dS_in is None and return_dstate:
             dS_in = torch.empty((B, Hkv, D, D), dtype=torch.float32, device=q.device)
         ws, ws_bytes = _scratch("la_backward_gated", lib.la_workspace_size_gated(
-            LA_OP_BACKWARD, B, H, Hkv, N, D, DTYPE[q.dtype]), workspace, q.device)
-        st = lib.la_backward_gated(_ptr(q), _ptr(k), _ptr(v), _ptr(log_gate), _ptr(dO),
+            LA_OP_BACKWARD, B, H, Hkv, N, D, code), workspace, q.device)
+        st = lib.la_backward_gated(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_gate.data_ptr(), _ptr(dO),
                                    _ptr(S_in), _ptr(dS_out), _ptr(dq), _ptr(dk), _ptr(dv),
                                    _ptr(dlog_gate), _ptr(dS_in), scale, B, H, Hkv, N, D,
-                                   DTYPE[q.dtype], _ptr(ws), ws_bytes, handle)
+                                   code, _ptr(ws), ws_bytes, handle)
     _check("la_backward_gated", st)
     return (dq, dk, dv, dlog_gate, dS_in) if return_dstate else (dq, dk, dv, dlog_gate)
 
@@ -646,27 +668,25 @@ def la_decode_step_gated(S, q, k, v, log_gate, scale: float = 1.0, o=None, strea
     k v^T, then o = scale S^T q; q [B, H, D], k, v [B, Hkv, D], log_gate
     [B, Hkv].  Returns o."""
     lib = load_library()
-    _check_qkv("la_decode_step_gated", q)
-    if q.dim() != 3:
-        raise ValueError("la_decode_step_gated: q must be [B, H, D], k and v [B, Hkv, D]")
-    Hkv = _check_kv("la_decode_step_gated", q, k, v)
-    B, H, D = q.shape
-    _check_like("la_decode_step_gated", "log_gate", log_gate, q, (B, Hkv))
+    B, H, Hkv, _, D, code = _check_gated("la_decode_step_gated", q, k, v, log_gate, 3)
     _check_like("la_decode_step_gated", "S", S, q, (B, Hkv, D, D), torch.float32)
     if o is not None:
         _check_qkv("la_decode_step_gated", q, o)
     with _LaunchOn(q, stream) as handle:
         o = torch.empty_like(q) if o is None else o
-        st = lib.la_decode_step_gated(_ptr(S), _ptr(q), _ptr(k), _ptr(v), _ptr(log_gate), _ptr(o),
-                                      scale, B, H, Hkv, D, DTYPE[q.dtype], handle)
+        st = lib.la_decode_step_gated(_ptr(S), q.data_ptr(), k.data_ptr(), v.data_ptr(), log_gate.data_ptr(), o.data_ptr(),
+                                      scale, B, H, Hkv, D, code, handle)
     _check("la_decode_step_gated", st)
     return o
 
 
 def _check_norm(name, x, weight, bias, gate, act):
-    _check_qkv(name, x)
-    if x.dim() != 4:
-        raise ValueError(f"{name}: x must be [B, H, N, D]")
+    if not x.is_cuda:
+        raise ValueError(f"{name}: tensors must be on a CUDA device")
+    if x.dtype not in DTYPE:
+        raise ValueError(f"{name}: dtype must be float32 or bfloat16, got {x.dtype}")
+    if x.dim() != 4 or not x.is_contiguous():
+        raise ValueError(f"{name}: x must be contiguous [B, H, N, D]")
     if act not in ACT:
         raise ValueError(f"{name}: act must be 'identity' or 'silu', got {act!r}")
     B, H, N, D = x.shape
