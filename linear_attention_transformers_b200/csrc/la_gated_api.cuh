@@ -3,6 +3,7 @@
 // and launches.  Included by la_api.cu, whose checks and helpers it uses.
 #pragma once
 
+#include "la_gated_bwd64.cuh"
 #include "la_gated_decode.cuh"
 #include "la_gated_generic.cuh"
 #include "la_gated_tc.cuh"
@@ -58,7 +59,11 @@ GatedTcPlan plan_gated_tc(la_op op, int64_t B, int64_t H, int64_t Hkv, int64_t N
     // tokens, 32 heads, forward: 2161 us with one, 1952 with two, 2083 with
     // four), D = 64, whose states are a quarter, does not (8192 tokens, 128
     // heads, backward: 883, 1026, 1169 us).
-    p.nb = p.nblk <= 1 ? 1 : p.nblk == 2 ? 2 : p.nblk <= 4 ? 4 : D == 64 ? 1 : 2;
+    // The backward kernel of D = 64 takes single blocks.
+    if (op == LA_OP_BACKWARD && D == 64)
+        p.nb = 1;
+    else
+        p.nb = p.nblk <= 1 ? 1 : p.nblk == 2 ? 2 : p.nblk <= 4 ? 4 : D == 64 ? 1 : 2;
     p.nspan = int((p.nblk + p.nb - 1) / p.nb);
     size_t at = 0;
     auto take = [&](size_t n) {
@@ -71,8 +76,10 @@ GatedTcPlan plan_gated_tc(la_op op, int64_t B, int64_t H, int64_t Hkv, int64_t N
     p.tot = take(size_t(B) * size_t(Hkv) * size_t(p.nspan) * 4);
     p.s_enter = take(states * 2);
     if (op == LA_OP_BACKWARD) {
-        const size_t qt = size_t(B) * size_t(H) * size_t(N) * 4;
         p.r_enter = take(states * 2);
+    }
+    if (op == LA_OP_BACKWARD && D != 64) {  // dlog_gate's pieces
+        const size_t qt = size_t(B) * size_t(H) * size_t(N) * 4;
         p.qrow = take(2 * qt);
         p.krow = take(size_t(B) * size_t(Hkv) * size_t(N) * 8);
         p.colv = take(qt * size_t(4 * p.nb));
@@ -258,18 +265,42 @@ la_status run_gated_bwd_tc(const void* q, const void* k, const void* v, const vo
     const int group = int(H / Hkv);
     const int64_t kvh = B * Hkv, qh = B * H;
     const void *S = nullptr, *R = nullptr;
-    if (p.nspan > 1 || S_in) {
+    // the backward of D = 64 takes both states or none
+    const bool both = D == 64 && (p.nspan > 1 || S_in || dS_out);
+    if (p.nspan > 1 || S_in || both) {
         S = ws + p.s_enter;
         if ((s = gated_tc_states<D, false>(k, v, lg, p, ws, p.s_enter, S_in, nullptr, kvh, kvh, N,
                                            1, 1.f, st)) != LA_OK)
             return s;
     }
-    if (p.nspan > 1 || dS_out || dS_in) {
+    if (p.nspan > 1 || dS_out || dS_in || both) {
         if ((s = gated_tc_states<D, true>(q, dO, lg, p, ws, p.r_enter, dS_out, dS_in, qh, kvh, N,
                                           group, scale, st)) != LA_OK)
             return s;
-        if (p.nspan > 1 || dS_out) R = ws + p.r_enter;
+        if (p.nspan > 1 || dS_out || both) R = ws + p.r_enter;
     }
+    if constexpr (D == 64) {
+        la::GatedBwd64Params prm;
+        memset(&prm, 0, sizeof(prm));
+        constexpr int C = la::kGtC;
+        if (!make_qkv_map(&prm.tm_q, q, qh, N, D, C) || !make_qkv_map(&prm.tm_k, k, kvh, N, D, C) ||
+            !make_qkv_map(&prm.tm_v, v, kvh, N, D, C) || !make_qkv_map(&prm.tm_do, dO, qh, N, D, C) ||
+            !make_qkv_map(&prm.tm_dq, dq, qh, N, D, C) ||
+            !make_qkv_map(&prm.tm_dk, dk, kvh, N, D, C) ||
+            !make_qkv_map(&prm.tm_dv, dv, kvh, N, D, C) ||
+            (both && (!make_qkv_map(&prm.tm_s, S, kvh * p.nspan, D, D, D) ||
+                      !make_qkv_map(&prm.tm_r, R, kvh * p.nspan, D, D, D))))
+            return LA_ERR_CUDA;
+        prm.lg = static_cast<const __nv_bfloat16*>(lg), prm.dlg = static_cast<__nv_bfloat16*>(dlg);
+        prm.N = N, prm.items = kvh * p.nblk, prm.nblk = int(p.nblk), prm.group = group;
+        prm.scale = scale;
+        auto kern = both ? la::gated_bwd64_kernel<true> : la::gated_bwd64_kernel<false>;
+        if ((s = allow_smem(kern, la::GatedBwd64Cfg::SMEM)) != LA_OK) return s;
+        la::LaunchScope scope("gated_bwd64", st);
+        kern<<<unsigned(std::min<int64_t>(prm.items, num_sms())), la::kGatedBwd64Threads,
+               la::GatedBwd64Cfg::SMEM, st>>>(prm);
+        return launch_status();
+    } else {
     float* qrow = reinterpret_cast<float*>(ws + p.qrow);
     float* krow = reinterpret_cast<float*>(ws + p.krow);
     float* colv = reinterpret_cast<float*>(ws + p.colv);
@@ -291,6 +322,7 @@ la_status run_gated_bwd_tc(const void* q, const void* k, const void* v, const vo
     la::LaunchScope scope("gated_dgate_sum", st);
     la::gated_dgate_sum_kernel<D><<<unsigned(kvh * p.nspan), 256, 0, st>>>(g);
     return launch_status();
+    }
 }
 
 template <typename T, int D>

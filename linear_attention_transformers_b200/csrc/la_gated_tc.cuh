@@ -45,6 +45,56 @@ struct alignas(16) GateTab {
     double start[4 * kGtMaxNb + 2];  // sums before each 32-token sub-block; [nsub] = all
 };
 
+// MMAs issued by one lane of a warp that runs the issue loop together: the
+// descriptors stay warp-uniform values and only the instruction is predicated.
+// Inside `if (lane == 0)` the issuing thread needs more instructions an MMA
+// (131072 tokens, D = 128, forward blocks: 1554 us, 1368 this way on the same
+// GPU), and in gated_bwd64_kernel, with its many tiles, 180 cycles an MMA
+// against 45 to 60.
+__device__ __forceinline__ void umma_one(uint32_t one, uint32_t d_tmem, uint64_t adesc,
+                                         uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(one)
+        : "memory");
+}
+__device__ __forceinline__ void umma_ts_one(uint32_t one, uint32_t d_tmem, uint32_t a_tmem,
+                                            uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(one)
+        : "memory");
+}
+__device__ __forceinline__ void commit_one(uint32_t one, uint64_t* bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}\n" ::
+            "r"(sm100::smem_u32(bar)),
+        "r"(one)
+        : "memory");
+}
+// One lane of the (converged) warp, the same one every time.
+__device__ __forceinline__ uint32_t elect_lane() {
+    uint32_t one;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(one));
+    return one;
+}
+// All lanes wait; false for all when one of the waits gave up.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+    return __all_sync(0xffffffffu, sm100::mbar_wait(bar, parity, abort));
+}
+
 __device__ __forceinline__ float ex2_fast(float x) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -201,7 +251,8 @@ gated_span_kernel(const __grid_constant__ GatedSpanParams prm) {
                 mbar_wait_drain(&full[i % NS], (i / NS) & 1);
         }
     } else if (warp == 1) {
-        if (lane == 0) {
+        {
+            const uint32_t one = elect_lane();
             constexpr uint32_t id = idesc_bf16(D, 2 * D, 1, 1);
             const uint64_t dsc = desc_mn_base(sbase + Cfg::OFF_SC, C);
             uint32_t n = 0, blk = 0, m = 0;
@@ -209,24 +260,24 @@ gated_span_kernel(const __grid_constant__ GatedSpanParams prm) {
             for (int64_t it = blockIdx.x; ok && it < items; it += gridDim.x, ++m) {
                 const int cnt = ng * blocks_of(span_of(it));
                 const uint32_t acc = tmem + (m & 1) * Cfg::ACC;
-                if (m >= 2 && !(ok = mbar_wait(&acc_free[m & 1], ((m >> 1) - 1) & 1, abort_flag)))
+                if (m >= 2 && !(ok = warp_wait(&acc_free[m & 1], ((m >> 1) - 1) & 1, abort_flag)))
                     break;
                 for (int b = 0; b < cnt; ++b, ++blk, n += 2) {
                     const int s = (n + 1) % NS;
-                    if (!(ok = mbar_wait(&full[s], ((n + 1) / NS) & 1, abort_flag))) break;
-                    if (!(ok = mbar_wait(sc_full, blk & 1, abort_flag))) break;
+                    if (!(ok = warp_wait(&full[s], ((n + 1) / NS) & 1, abort_flag))) break;
+                    if (!(ok = warp_wait(sc_full, blk & 1, abort_flag))) break;
                     tc_fence_after();
                     const uint64_t db = desc_mn_base(sbase + s * Cfg::TILE, C);
 #pragma unroll
                     for (int k = 0; k < C; k += 16)
-                        umma_bf16(acc, db + kstep_mn(k), dsc + kstep_mn(k), id, b > 0 || k > 0);
-                    umma_commit(&empty[s]);
-                    umma_commit(sc_free);
+                        umma_one(one, acc, db + kstep_mn(k), dsc + kstep_mn(k), id, b > 0 || k > 0);
+                    commit_one(one, &empty[s]);
+                    commit_one(one, sc_free);
                 }
-                if (ok) umma_commit(&acc_full[m & 1]);
+                if (ok) commit_one(one, &acc_full[m & 1]);
             }
-            umma_commit(drain);
-            mbar_wait_drain(drain, 0);
+            commit_one(one, drain);
+            if (lane == 0) mbar_wait_drain(drain, 0);
         }
     } else if (warp == 2) {
         uint32_t m = 0;
@@ -549,7 +600,8 @@ gated_block_kernel(const __grid_constant__ GatedBlockParams prm) {
                 mbar_wait_drain(&full[i % NS], (i / NS) & 1);
         }
     } else if (warp == 1) {
-        if (lane == 0) {
+        {
+            const uint32_t one = elect_lane();
             constexpr uint32_t idP = idesc_bf16(C, C, 0, 0);             // rows x columns
             constexpr uint32_t idS = idesc_bf16(C, D, 0, TRANS ? 0 : 1); // rows through S or S^T
             constexpr uint32_t idV = idesc_bf16(C, D, 0, 1);             // weighted P, values
@@ -557,7 +609,7 @@ gated_block_kernel(const __grid_constant__ GatedBlockParams prm) {
             bool ok = true;
             auto tile = [&](uint32_t i) { return sbase + (i % NS) * Cfg::TILE; };
             auto landed = [&](uint32_t i) {
-                return mbar_wait(&full[i % NS], (i / NS) & 1, abort_flag);
+                return warp_wait(&full[i % NS], (i / NS) & 1, abort_flag);
             };
             for (int64_t it = blockIdx.x; ok && it < prm.items; it += gridDim.x, ++m) {
                 const Item x = item_of(it);
@@ -570,9 +622,9 @@ gated_block_kernel(const __grid_constant__ GatedBlockParams prm) {
                 // P of column block b, into the buffer that block b - NP is done with
                 auto p_part = [&](int b) {
                     const uint32_t i = pc + b, buf = i % NP;
-                    if (i >= NP && !mbar_wait(&p_free[buf], (i / NP - 1) & 1, abort_flag))
+                    if (i >= NP && !warp_wait(&p_free[buf], (i / NP - 1) & 1, abort_flag))
                         return false;
-                    if (b == 0 && !mbar_wait(&row_full[rbuf], (m / Cfg::NR) & 1, abort_flag))
+                    if (b == 0 && !warp_wait(&row_full[rbuf], (m / Cfg::NR) & 1, abort_flag))
                         return false;
                     if (!landed(col_at(b))) return false;
                     if (XTRA == 2 && !landed(val_at(b))) return false;
@@ -580,40 +632,40 @@ gated_block_kernel(const __grid_constant__ GatedBlockParams prm) {
                     const uint64_t dcol = desc_k_base(tile(col_at(b)));
 #pragma unroll
                     for (int k = 0; k < D; k += 16)
-                        umma_bf16(tmem + Cfg::T_P + buf * C, drow + kstep_k(C, k),
+                        umma_one(one, tmem + Cfg::T_P + buf * C, drow + kstep_k(C, k),
                                   dcol + kstep_k(C, k), idP, k > 0);
                     if constexpr (XTRA == 2) {
                         const uint64_t dr2 = desc_k_base(row + Cfg::TILE),
                                        dv = desc_k_base(tile(val_at(b)));
 #pragma unroll
                         for (int k = 0; k < D; k += 16)
-                            umma_bf16(tmem + Cfg::T_P2, dr2 + kstep_k(C, k), dv + kstep_k(C, k),
+                            umma_one(one, tmem + Cfg::T_P2, dr2 + kstep_k(C, k), dv + kstep_k(C, k),
                                       idP, k > 0);
                     }
-                    umma_commit(&p_full[buf]);
-                    umma_commit(&empty[col_at(b) % NS]);
+                    commit_one(one, &p_full[buf]);
+                    commit_one(one, &empty[col_at(b) % NS]);
                     return true;
                 };
                 if (!(ok = p_part(0))) break;
-                if (m > 0 && !(ok = mbar_wait(o_free, (m - 1) & 1, abort_flag))) break;
+                if (m > 0 && !(ok = warp_wait(o_free, (m - 1) & 1, abort_flag))) break;
                 if (hs) {
                     if (!(ok = landed(st))) break;
                     tc_fence_after();
                     const uint64_t ds = TRANS ? desc_k_base(tile(st)) : desc_mn_base(tile(st), D);
 #pragma unroll
                     for (int k = 0; k < D; k += 16)
-                        umma_bf16(tmem + Cfg::T_ST, drow + kstep_k(C, k),
+                        umma_one(one, tmem + Cfg::T_ST, drow + kstep_k(C, k),
                                   ds + (TRANS ? kstep_k(D, k) : kstep_mn(k)), idS, k > 0);
-                    umma_commit(&empty[st % NS]);
+                    commit_one(one, &empty[st % NS]);
                 }
-                if (x.ncb == 1) umma_commit(&row_free[rbuf]);
+                if (x.ncb == 1) commit_one(one, &row_free[rbuf]);
                 for (int b = 0; b < x.ncb; ++b) {
                     if (NP == 2 && b + 1 < x.ncb) {
                         if (!(ok = p_part(b + 1))) break;
-                        if (b + 2 == x.ncb) umma_commit(&row_free[rbuf]);
+                        if (b + 2 == x.ncb) commit_one(one, &row_free[rbuf]);
                     }
                     const uint32_t i = pc + b;
-                    if (!(ok = mbar_wait(&pt_full[i % NP], (i / NP) & 1, abort_flag))) break;
+                    if (!(ok = warp_wait(&pt_full[i % NP], (i / NP) & 1, abort_flag))) break;
                     if (!(ok = landed(val_at(b)))) break;
                     tc_fence_after();
                     const uint32_t tp = tmem + Cfg::T_P + (i % NP) * C;
@@ -621,23 +673,23 @@ gated_block_kernel(const __grid_constant__ GatedBlockParams prm) {
                     // packed halves: columns 0.. and 64.. of the buffer
 #pragma unroll
                     for (int k = 0; k < C; k += 16)
-                        umma_bf16_ts(tmem + Cfg::T_IN, tp + (k < 64 ? k / 2 : 32 + k / 2),
+                        umma_ts_one(one, tmem + Cfg::T_IN, tp + (k < 64 ? k / 2 : 32 + k / 2),
                                      dv + kstep_mn(k), idV, b > 0 || k > 0);
-                    umma_commit(&p_free[i % NP]);
+                    commit_one(one, &p_free[i % NP]);
                     if (b + 1 < x.ncb)
-                        umma_commit(&empty[val_at(b) % NS]);  // the last one: the store warp
+                        commit_one(one, &empty[val_at(b) % NS]);  // the last one: the store warp
                     else
-                        umma_commit(o_full);
+                        commit_one(one, o_full);
                     if (NP == 1 && b + 1 < x.ncb) {
                         if (!(ok = p_part(b + 1))) break;
-                        if (b + 2 == x.ncb) umma_commit(&row_free[rbuf]);
+                        if (b + 2 == x.ncb) commit_one(one, &row_free[rbuf]);
                     }
                 }
                 pc += x.ncb;
                 n += x.loads;
             }
-            umma_commit(drain);
-            mbar_wait_drain(drain, 0);
+            commit_one(one, drain);
+            if (lane == 0) mbar_wait_drain(drain, 0);
         }
     } else if (warp == 2) {
         uint32_t m = 0, issued = 0;
