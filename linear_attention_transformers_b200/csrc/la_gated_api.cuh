@@ -4,6 +4,7 @@
 #pragma once
 
 #include "la_gated_bwd64.cuh"
+#include "la_gated_chain.cuh"
 #include "la_gated_decode.cuh"
 #include "la_gated_generic.cuh"
 #include "la_gated_tc.cuh"
@@ -47,8 +48,23 @@ GatedPlan plan_gated(la_op op, int64_t B, int64_t Hkv, int64_t N, int64_t D) {
 struct GatedTcPlan {
     int64_t nblk = 0;
     int nb = 0, nspan = 0;
+    int chain = 0;  // value columns a CTA of the walk takes; 0: spans in parallel
     size_t rec = 0, tot = 0, s_enter = 0, r_enter = 0, qrow = 0, krow = 0, colv = 0, bytes = 0;
 };
+
+// How the border states are formed: spans in parallel (0; two launches and the
+// float32 records) or a walk of CTAs of 64 or 32 value columns, whichever the
+// model below says is sooner, in us.  Measured (spans; walk with 64; with 32):
+// 128 heads of 8192 tokens, D = 64: 117, 97, 117; 64 of 4096, D = 128: 61, 54,
+// 65; 32 of 131072, D = 128: 811, 1435, 904; 8 of 777, D = 128: 20, 21, 15.
+int pick_chain(int64_t kvh, int64_t nblk, int64_t D) {
+    const double sms = num_sms();
+    const double spans = 10.0 + double(kvh) * double(nblk) * (D == 64 ? 0.0134 : 0.0243);
+    const double w64 = 4.0 + ceil(double(kvh) * double(D / 64) / sms) * double(nblk) * 1.5;
+    const double w32 = 4.0 + ceil(double(kvh) * double(D / 32) / sms) * double(nblk) * 0.9;
+    if (spans <= w64 && spans <= w32) return 0;
+    return w64 <= w32 ? 64 : 32;
+}
 
 GatedTcPlan plan_gated_tc(la_op op, int64_t B, int64_t H, int64_t Hkv, int64_t N, int64_t D) {
     GatedTcPlan p;
@@ -65,6 +81,7 @@ GatedTcPlan plan_gated_tc(la_op op, int64_t B, int64_t H, int64_t Hkv, int64_t N
     else
         p.nb = p.nblk <= 1 ? 1 : p.nblk == 2 ? 2 : p.nblk <= 4 ? 4 : D == 64 ? 1 : 2;
     p.nspan = int((p.nblk + p.nb - 1) / p.nb);
+    p.chain = pick_chain(B * Hkv, p.nblk, D);
     size_t at = 0;
     auto take = [&](size_t n) {
         const size_t o = at;
@@ -72,8 +89,10 @@ GatedTcPlan plan_gated_tc(la_op op, int64_t B, int64_t H, int64_t Hkv, int64_t N
         return o;
     };
     const size_t states = size_t(B) * size_t(Hkv) * size_t(p.nspan) * size_t(D * D);
-    p.rec = take(states * 4);
-    p.tot = take(size_t(B) * size_t(Hkv) * size_t(p.nspan) * 4);
+    if (!p.chain) {
+        p.rec = take(states * 4);
+        p.tot = take(size_t(B) * size_t(Hkv) * size_t(p.nspan) * 4);
+    }
     p.s_enter = take(states * 2);
     if (op == LA_OP_BACKWARD) {
         p.r_enter = take(states * 2);
@@ -162,11 +181,40 @@ la_status gated_rows(const char* name, const T* R, const T* K, const T* V, const
 }
 
 // ---------------------------------------------------- the tensor-core kernels
+template <int D, int EC, bool REV>
+la_status gated_tc_chain(const void* A, const void* Bm, const void* lg, const GatedTcPlan& p,
+                         char* ws, size_t enter, const float* first, float* last, int64_t heads,
+                         int64_t kvh, int64_t N, int group, float mul, cudaStream_t st) {
+    using Cfg = la::GatedChainCfg<D, EC>;
+    la_status s;
+    la::GatedChainParams prm;
+    memset(&prm, 0, sizeof(prm));
+    if (!make_qkv_map(&prm.tm_a, A, heads, N, D, la::kGtC)) return LA_ERR_CUDA;
+    prm.b = static_cast<const __nv_bfloat16*>(Bm), prm.lg = static_cast<const __nv_bfloat16*>(lg);
+    prm.first = first, prm.last = last;
+    prm.enter = reinterpret_cast<__nv_bfloat16*>(ws + enter);
+    prm.N = N, prm.nblk = int(p.nblk), prm.nb = p.nb, prm.nspan = p.nspan, prm.group = group;
+    prm.mul = mul;
+    // without `last` the span walked last adds nothing that is asked for
+    prm.blocks = last ? prm.nblk : REV ? std::max(0, prm.nblk - p.nb) : (p.nspan - 1) * p.nb;
+    auto kern = la::gated_chain_kernel<D, EC, REV>;
+    if ((s = allow_smem(kern, Cfg::SMEM)) != LA_OK) return s;
+    la::LaunchScope scope(REV ? "gated_chain_rev" : "gated_chain", st);
+    kern<<<unsigned(kvh * (D / EC)), la::kGatedChainThreads, Cfg::SMEM, st>>>(prm);
+    return launch_status();
+}
+
 template <int D, bool REV>
 la_status gated_tc_states(const void* A, const void* Bm, const void* lg, const GatedTcPlan& p,
                           char* ws, size_t enter, const float* first, float* last, int64_t heads,
                           int64_t kvh, int64_t N, int group, float mul, cudaStream_t st) {
     la_status s;
+    if (p.chain == 32)
+        return gated_tc_chain<D, 32, REV>(A, Bm, lg, p, ws, enter, first, last, heads, kvh, N,
+                                          group, mul, st);
+    if (p.chain)
+        return gated_tc_chain<D, 64, REV>(A, Bm, lg, p, ws, enter, first, last, heads, kvh, N,
+                                          group, mul, st);
     const int run = last ? p.nspan : p.nspan - 1;
     float* rec = reinterpret_cast<float*>(ws + p.rec);
     float* tot = reinterpret_cast<float*>(ws + p.tot);

@@ -190,7 +190,8 @@ def test_rows_behind_the_last_are_left(D):
 
 @pytest.mark.parametrize("D", [32, 64, 128])
 def test_long_offsets(D):
-    # tensors of more than 2^31 elements: the last heads equal a call on them alone
+    # tensors of more than 2^31 elements: the last heads are those of a call on them
+    # alone (up to its own rounding: the states may be formed another way there)
     dtype = torch.bfloat16
     N, H = 4096, (1 << 31) // (4096 * D) + 3
     g = torch.Generator(device="cuda").manual_seed(1)
@@ -199,7 +200,8 @@ def test_long_offsets(D):
     o, S = api.la_forward_gated(q, q, q, lg, return_state=True)
     a, b = (q[:, -2:].contiguous(), lg[:, -2:].contiguous())
     o2, S2 = api.la_forward_gated(a, a, a, b, return_state=True)
-    assert torch.equal(o[:, -2:], o2) and torch.equal(S[:, -2:], S2)
+    close(o[:, -2:], o2.double().cpu(), 2 * REL[dtype], 2 * MAX[dtype], "o")
+    close(S[:, -2:], S2.double().cpu(), 2 * REL_STATE[dtype], 8 * REL_STATE[dtype], "S")
 
 
 @pytest.mark.parametrize("D", [32, 64, 128])
