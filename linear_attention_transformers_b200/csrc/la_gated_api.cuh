@@ -3,7 +3,7 @@
 // and launches.  Included by la_api.cu, whose checks and helpers it uses.
 #pragma once
 
-#include "la_gated_bwd64.cuh"
+#include "la_gated_bwd.cuh"
 #include "la_gated_chain.cuh"
 #include "la_gated_decode.cuh"
 #include "la_gated_generic.cuh"
@@ -49,7 +49,7 @@ struct GatedTcPlan {
     int64_t nblk = 0;
     int nb = 0, nspan = 0;
     int chain = 0;  // value columns a CTA of the walk takes; 0: spans in parallel
-    size_t rec = 0, tot = 0, s_enter = 0, r_enter = 0, qrow = 0, krow = 0, colv = 0, bytes = 0;
+    size_t rec = 0, tot = 0, s_enter = 0, r_enter = 0, bytes = 0;
 };
 
 // How the border states are formed: spans in parallel (0; two launches and the
@@ -75,8 +75,8 @@ GatedTcPlan plan_gated_tc(la_op op, int64_t B, int64_t H, int64_t Hkv, int64_t N
     // tokens, 32 heads, forward: 2161 us with one, 1952 with two, 2083 with
     // four), D = 64, whose states are a quarter, does not (8192 tokens, 128
     // heads, backward: 883, 1026, 1169 us).
-    // The backward kernel of D = 64 takes single blocks.
-    if (op == LA_OP_BACKWARD && D == 64)
+    // The backward kernels take single blocks.
+    if (op == LA_OP_BACKWARD)
         p.nb = 1;
     else
         p.nb = p.nblk <= 1 ? 1 : p.nblk == 2 ? 2 : p.nblk <= 4 ? 4 : D == 64 ? 1 : 2;
@@ -96,12 +96,6 @@ GatedTcPlan plan_gated_tc(la_op op, int64_t B, int64_t H, int64_t Hkv, int64_t N
     p.s_enter = take(states * 2);
     if (op == LA_OP_BACKWARD) {
         p.r_enter = take(states * 2);
-    }
-    if (op == LA_OP_BACKWARD && D != 64) {  // dlog_gate's pieces
-        const size_t qt = size_t(B) * size_t(H) * size_t(N) * 4;
-        p.qrow = take(2 * qt);
-        p.krow = take(size_t(B) * size_t(Hkv) * size_t(N) * 8);
-        p.colv = take(qt * size_t(4 * p.nb));
     }
     p.bytes = at;
     return p;
@@ -312,65 +306,35 @@ la_status run_gated_bwd_tc(const void* q, const void* k, const void* v, const vo
     const GatedTcPlan p = plan_gated_tc(LA_OP_BACKWARD, B, H, Hkv, N, D);
     const int group = int(H / Hkv);
     const int64_t kvh = B * Hkv, qh = B * H;
-    const void *S = nullptr, *R = nullptr;
-    // the backward of D = 64 takes both states or none
-    const bool both = D == 64 && (p.nspan > 1 || S_in || dS_out);
-    if (p.nspan > 1 || S_in || both) {
-        S = ws + p.s_enter;
-        if ((s = gated_tc_states<D, false>(k, v, lg, p, ws, p.s_enter, S_in, nullptr, kvh, kvh, N,
-                                           1, 1.f, st)) != LA_OK)
-            return s;
-    }
-    if (p.nspan > 1 || dS_out || dS_in || both) {
-        if ((s = gated_tc_states<D, true>(q, dO, lg, p, ws, p.r_enter, dS_out, dS_in, qh, kvh, N,
-                                          group, scale, st)) != LA_OK)
-            return s;
-        if (p.nspan > 1 || dS_out || both) R = ws + p.r_enter;
-    }
-    if constexpr (D == 64) {
-        la::GatedBwd64Params prm;
-        memset(&prm, 0, sizeof(prm));
-        constexpr int C = la::kGtC;
-        if (!make_qkv_map(&prm.tm_q, q, qh, N, D, C) || !make_qkv_map(&prm.tm_k, k, kvh, N, D, C) ||
-            !make_qkv_map(&prm.tm_v, v, kvh, N, D, C) || !make_qkv_map(&prm.tm_do, dO, qh, N, D, C) ||
-            !make_qkv_map(&prm.tm_dq, dq, qh, N, D, C) ||
-            !make_qkv_map(&prm.tm_dk, dk, kvh, N, D, C) ||
-            !make_qkv_map(&prm.tm_dv, dv, kvh, N, D, C) ||
-            (both && (!make_qkv_map(&prm.tm_s, S, kvh * p.nspan, D, D, D) ||
-                      !make_qkv_map(&prm.tm_r, R, kvh * p.nspan, D, D, D))))
-            return LA_ERR_CUDA;
-        prm.lg = static_cast<const __nv_bfloat16*>(lg), prm.dlg = static_cast<__nv_bfloat16*>(dlg);
-        prm.N = N, prm.items = kvh * p.nblk, prm.nblk = int(p.nblk), prm.group = group;
-        prm.scale = scale;
-        auto kern = both ? la::gated_bwd64_kernel<true> : la::gated_bwd64_kernel<false>;
-        if ((s = allow_smem(kern, la::GatedBwd64Cfg::SMEM)) != LA_OK) return s;
-        la::LaunchScope scope("gated_bwd64", st);
-        kern<<<unsigned(std::min<int64_t>(prm.items, num_sms())), la::kGatedBwd64Threads,
-               la::GatedBwd64Cfg::SMEM, st>>>(prm);
-        return launch_status();
-    } else {
-    float* qrow = reinterpret_cast<float*>(ws + p.qrow);
-    float* krow = reinterpret_cast<float*>(ws + p.krow);
-    float* colv = reinterpret_cast<float*>(ws + p.colv);
-    const GatedBlockCall cq{"gated_dq", dO, v, k, q, S, dq, qrow, colv, qh, kvh, kvh, scale, scale};
-    if ((s = gated_tc_block<D, false, true, 2>(cq, lg, p, N, group, st)) != LA_OK) return s;
-    const GatedBlockCall ck{"gated_dk", v, dO, q, k, R, dk, krow, nullptr, kvh, qh, kvh, scale, 1.f};
-    s = R ? gated_tc_block<D, true, true, 1>(ck, lg, p, N, group, st)
-          : gated_tc_block<D, true, true, 0>(ck, lg, p, N, group, st);
-    if (s != LA_OK) return s;
-    const GatedBlockCall cv{"gated_dv", k, q, dO, nullptr, R, dv, nullptr, nullptr, kvh, qh, kvh,
-                            scale, 1.f};
-    if ((s = gated_tc_block<D, true, false, 0>(cv, lg, p, N, group, st)) != LA_OK) return s;
-    la::GatedDgateParams g{};
-    g.qrow = qrow, g.colv = colv, g.krow = R ? krow : nullptr;
-    g.S = static_cast<const __nv_bfloat16*>(S), g.R = static_cast<const __nv_bfloat16*>(R);
-    g.lg = static_cast<const __nv_bfloat16*>(lg), g.dlg = static_cast<__nv_bfloat16*>(dlg);
-    g.N = N, g.qheads = qh, g.kvh = kvh;
-    g.nspan = p.nspan, g.nb = p.nb, g.nblk = int(p.nblk), g.group = group;
-    la::LaunchScope scope("gated_dgate_sum", st);
-    la::gated_dgate_sum_kernel<D><<<unsigned(kvh * p.nspan), 256, 0, st>>>(g);
+    // the blocks take both border states or, a single block that nothing enters
+    // or leaves, none
+    const bool state = p.nspan > 1 || S_in || dS_out;
+    if (state && (s = gated_tc_states<D, false>(k, v, lg, p, ws, p.s_enter, S_in, nullptr, kvh, kvh,
+                                                N, 1, 1.f, st)) != LA_OK)
+        return s;
+    if ((state || dS_in) &&
+        (s = gated_tc_states<D, true>(q, dO, lg, p, ws, p.r_enter, dS_out, dS_in, qh, kvh, N, group,
+                                      scale, st)) != LA_OK)
+        return s;
+    la::GatedBwdParams prm;
+    memset(&prm, 0, sizeof(prm));
+    constexpr int C = la::kGtC;
+    if (!make_qkv_map(&prm.tm_q, q, qh, N, D, C) || !make_qkv_map(&prm.tm_k, k, kvh, N, D, C) ||
+        !make_qkv_map(&prm.tm_v, v, kvh, N, D, C) || !make_qkv_map(&prm.tm_do, dO, qh, N, D, C) ||
+        !make_qkv_map(&prm.tm_dq, dq, qh, N, D, C) || !make_qkv_map(&prm.tm_dk, dk, kvh, N, D, C) ||
+        !make_qkv_map(&prm.tm_dv, dv, kvh, N, D, C) ||
+        (state && (!make_qkv_map(&prm.tm_s, ws + p.s_enter, kvh * p.nspan, D, D, D) ||
+                   !make_qkv_map(&prm.tm_r, ws + p.r_enter, kvh * p.nspan, D, D, D))))
+        return LA_ERR_CUDA;
+    prm.lg = static_cast<const __nv_bfloat16*>(lg), prm.dlg = static_cast<__nv_bfloat16*>(dlg);
+    prm.N = N, prm.items = kvh * p.nblk, prm.nblk = int(p.nblk), prm.group = group;
+    prm.scale = scale;
+    auto kern = state ? la::gated_bwd_kernel<D, true> : la::gated_bwd_kernel<D, false>;
+    constexpr size_t kSmem = la::GatedBwdCfg<D>::SMEM;
+    if ((s = allow_smem(kern, kSmem)) != LA_OK) return s;
+    la::LaunchScope scope("gated_bwd", st);
+    kern<<<unsigned(std::min<int64_t>(prm.items, num_sms())), la::kGatedBwdThreads, kSmem, st>>>(prm);
     return launch_status();
-    }
 }
 
 template <typename T, int D>
