@@ -241,44 +241,6 @@ la_status gated_tc_states(const void* A, const void* Bm, const void* lg, const G
     return launch_status();
 }
 
-// rows, columns, values, second rows (XTRA), states entering the spans (null:
-// none), output; `heads` row heads, `colh` column heads
-struct GatedBlockCall {
-    const char* name;
-    const void *row, *col, *val, *row2, *state;
-    void* out;
-    float *rowv, *colv;
-    int64_t heads, colh, kvh;
-    float in_mul, st_mul;
-};
-
-template <int D, bool REV, bool TRANS, int XTRA>
-la_status gated_tc_block(const GatedBlockCall& c, const void* lg, const GatedTcPlan& p, int64_t N,
-                         int group, cudaStream_t st) {
-    using Cfg = la::GatedBlockCfg<D, XTRA>;
-    la_status s;
-    la::GatedBlockParams prm;
-    memset(&prm, 0, sizeof(prm));
-    if (!make_qkv_map(&prm.tm_row, c.row, c.heads, N, D, la::kGtC) ||
-        !make_qkv_map(&prm.tm_col, c.col, c.colh, N, D, la::kGtC) ||
-        !make_qkv_map(&prm.tm_val, c.val, c.colh, N, D, la::kGtC) ||
-        !make_qkv_map(&prm.tm_out, c.out, c.heads, N, D, la::kGtC) ||
-        (XTRA && !make_qkv_map(&prm.tm_row2, c.row2, c.heads, N, D, la::kGtC)) ||
-        (c.state && !make_qkv_map(&prm.tm_st, c.state, c.kvh * p.nspan, D, D, D)))
-        return LA_ERR_CUDA;
-    prm.lg = static_cast<const __nv_bfloat16*>(lg);
-    prm.rowv = c.rowv, prm.colv = c.colv, prm.N = N;
-    prm.items = c.heads * p.nblk, prm.heads = c.heads;
-    prm.nblk = int(p.nblk), prm.nb = p.nb, prm.nspan = p.nspan, prm.group = group;
-    prm.has_state = c.state != nullptr, prm.in_mul = c.in_mul, prm.st_mul = c.st_mul;
-    auto kern = la::gated_block_kernel<D, REV, TRANS, XTRA>;
-    if ((s = allow_smem(kern, Cfg::SMEM)) != LA_OK) return s;
-    const unsigned grid = unsigned(std::min<int64_t>(prm.items, int64_t(num_sms()) * Cfg::CTAS));
-    la::LaunchScope scope(c.name, st);
-    kern<<<grid, la::kGatedBlockThreads, Cfg::SMEM, st>>>(prm);
-    return launch_status();
-}
-
 template <int D>
 la_status run_gated_fwd_tc(const void* q, const void* k, const void* v, const void* lg, void* o,
                            const float* S_in, float* S_out, float scale, int64_t B, int64_t H,
@@ -292,9 +254,25 @@ la_status run_gated_fwd_tc(const void* q, const void* k, const void* v, const vo
         if (s != LA_OK) return s;
     }
     const bool state = p.nspan > 1 || S_in;
-    const GatedBlockCall c{"gated_o", q, k, v, nullptr, state ? ws + p.s_enter : nullptr, o,
-                           nullptr, nullptr, B * H, kvh, kvh, scale, scale};
-    return gated_tc_block<D, false, false, 0>(c, lg, p, N, int(H / Hkv), st);
+    using Cfg = la::GatedBlockCfg<D>;
+    la::GatedBlockParams prm;
+    memset(&prm, 0, sizeof(prm));
+    constexpr int C = la::kGtC;
+    if (!make_qkv_map(&prm.tm_q, q, B * H, N, D, C) || !make_qkv_map(&prm.tm_k, k, kvh, N, D, C) ||
+        !make_qkv_map(&prm.tm_v, v, kvh, N, D, C) || !make_qkv_map(&prm.tm_o, o, B * H, N, D, C) ||
+        (state && !make_qkv_map(&prm.tm_st, ws + p.s_enter, kvh * p.nspan, D, D, D)))
+        return LA_ERR_CUDA;
+    prm.lg = static_cast<const __nv_bfloat16*>(lg);
+    prm.N = N, prm.items = B * H * p.nblk;
+    prm.nblk = int(p.nblk), prm.nb = p.nb, prm.nspan = p.nspan, prm.group = int(H / Hkv);
+    prm.has_state = state, prm.scale = scale;
+    auto kern = la::gated_block_kernel<D>;
+    la_status s;
+    if ((s = allow_smem(kern, Cfg::SMEM)) != LA_OK) return s;
+    const unsigned grid = unsigned(std::min<int64_t>(prm.items, int64_t(num_sms()) * Cfg::CTAS));
+    la::LaunchScope scope("gated_o", st);
+    kern<<<grid, Cfg::THREADS, Cfg::SMEM, st>>>(prm);
+    return launch_status();
 }
 
 template <int D>

@@ -98,18 +98,18 @@ gated_bwd_kernel(const __grid_constant__ GatedBwdParams prm) {
     uint64_t* sr_full = bars + 8;    // TMA
     uint64_t* sr_free = bars + 9;    // S, R (D = 128: and P~, W~) read    (commit)
     uint64_t* pw_raw = bars + 10;    // P, W complete                      (commit)
-    uint64_t* p_read = bars + 11;    // P, W in registers; <S, R> formed   (512)
+    uint64_t* p_read = bars + 11;    // P, W in registers; <S, R> formed   (16 warps)
     uint64_t* s_full = bars + 12;    // products with S and R complete     (commit)
-    uint64_t* pw_full = bars + 13;   // P~, W~ packed, state parts scaled  (512)
+    uint64_t* pw_full = bars + 13;   // P~, W~ packed, state parts scaled  (16 warps)
     uint64_t* a_full = bars + 14;    // dq, dk complete                    (commit)
     uint64_t* b_full = bars + 15;    // dv complete                        (commit)
-    uint64_t* dq_read = bars + 16;   // dq accumulator read                (512)
-    uint64_t* kv_read = bars + 17;   // dk, dv accumulators read           (512)
-    uint64_t* dq_out = bars + 18;    // dq staged                          (512)
-    uint64_t* kv_out = bars + 19;    // dk, dv staged; dlog_gate's sums written (512)
-    uint64_t* red_free = bars + 20;  // ... read                           (32)
-    uint64_t* tab_full = bars + 21;  // [2] gate tables written            (32)
-    uint64_t* tab_free = bars + 23;  // [2] ... read                       (512)
+    uint64_t* dq_read = bars + 16;   // dq accumulator read                (16 warps)
+    uint64_t* kv_read = bars + 17;   // dk, dv accumulators read           (16 warps)
+    uint64_t* dq_out = bars + 18;    // dq staged                          (16 warps)
+    uint64_t* kv_out = bars + 19;    // dk, dv staged; dlog_gate's sums written (16 warps)
+    uint64_t* red_free = bars + 20;  // ... read                           (1)
+    uint64_t* tab_full = bars + 21;  // [2] gate tables written            (1)
+    uint64_t* tab_free = bars + 23;  // [2] ... read                       (16 warps)
     uint64_t* drain = bars + 25;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Cfg::OFF_MISC);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Cfg::OFF_MISC + 4);
@@ -127,19 +127,19 @@ gated_bwd_kernel(const __grid_constant__ GatedBwdParams prm) {
         mbar_init(sr_full, 1);
         mbar_init(sr_free, 1);
         mbar_init(pw_raw, 1);
-        mbar_init(p_read, kGatedBwdWork);
+        mbar_init(p_read, kGatedBwdWork / 32);
         mbar_init(s_full, 1);
-        mbar_init(pw_full, kGatedBwdWork);
+        mbar_init(pw_full, kGatedBwdWork / 32);
         mbar_init(a_full, 1);
         mbar_init(b_full, 1);
-        mbar_init(dq_read, kGatedBwdWork);
-        mbar_init(kv_read, kGatedBwdWork);
-        mbar_init(dq_out, kGatedBwdWork);
-        mbar_init(kv_out, kGatedBwdWork);
-        mbar_init(red_free, 32);
+        mbar_init(dq_read, kGatedBwdWork / 32);
+        mbar_init(kv_read, kGatedBwdWork / 32);
+        mbar_init(dq_out, kGatedBwdWork / 32);
+        mbar_init(kv_out, kGatedBwdWork / 32);
+        mbar_init(red_free, 1);
         for (int b = 0; b < 2; ++b) {
-            mbar_init(&tab_full[b], 32);
-            mbar_init(&tab_free[b], kGatedBwdWork);
+            mbar_init(&tab_full[b], 1);
+            mbar_init(&tab_free[b], kGatedBwdWork / 32);
         }
         mbar_init(drain, 1);
         *abort_flag = 0;
@@ -302,8 +302,7 @@ gated_bwd_kernel(const __grid_constant__ GatedBwdParams prm) {
                           tab.loc[t] = float(run - before);
                           tab.fac[t] = ex2_fast(float(end - run));
                       });
-            __syncwarp();
-            mbar_arrive(&tab_full[buf]);
+            warp_arrive(&tab_full[buf]);
         };
         uint32_t m = 0;
         if (int64_t(blockIdx.x) < prm.items) tables(blockIdx.x, 0);
@@ -333,8 +332,7 @@ gated_bwd_kernel(const __grid_constant__ GatedBwdParams prm) {
                 ds += d[j];
                 ts += t[j];
             }
-            __syncwarp();
-            mbar_arrive(red_free);
+            warp_arrive(red_free);
             float behind = ds, before = ts;  // sums over the lanes behind / before
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -513,7 +511,7 @@ gated_bwd_kernel(const __grid_constant__ GatedBwdParams prm) {
                     }
                 }
                 tc_fence_before();
-                mbar_arrive(p_read);
+                warp_arrive(p_read);
                 uint8_t* qt = smem + Cfg::OFF_QD + (u % NB) * 2 * TILE;
                 if (!(ok = wait(&qd_full[u % NB], (u / NB) & 1) &&
                            wait(&kv_full[m % NB], (m / NB) & 1)))
@@ -542,7 +540,7 @@ gated_bwd_kernel(const __grid_constant__ GatedBwdParams prm) {
                 }
                 fence_proxy_async_smem();
                 tc_fence_before();
-                mbar_arrive(pw_full);
+                warp_arrive(pw_full);
                 if (J <= sp) {  // M's sums while the products run
                     // rows and columns add the same rounded values, so what cancels
                     // between them still does
@@ -576,8 +574,8 @@ gated_bwd_kernel(const __grid_constant__ GatedBwdParams prm) {
                 put(Cfg::T_DQ, qt);
                 fence_proxy_async_smem();
                 tc_fence_before();
-                mbar_arrive(dq_read);
-                mbar_arrive(dq_out);
+                warp_arrive(dq_read);
+                warp_arrive(dq_out);
                 if (g == G - 1) put(Cfg::T_DK, kt);
                 if (!(ok = wait(b_full, u & 1))) break;
                 tc_fence_after();
@@ -594,9 +592,9 @@ gated_bwd_kernel(const __grid_constant__ GatedBwdParams prm) {
             if (lane == 0) red[12 * C + warp - 4] = sr;
             fence_proxy_async_smem();
             tc_fence_before();
-            mbar_arrive(kv_read);
-            mbar_arrive(kv_out);
-            mbar_arrive(&tab_free[m & 1]);
+            warp_arrive(kv_read);
+            warp_arrive(kv_out);
+            warp_arrive(&tab_free[m & 1]);
         }
     }
     tc_fence_before();

@@ -71,12 +71,12 @@ gated_chain_kernel(const __grid_constant__ GatedChainParams prm) {
     const uint32_t sbase = smem_u32(smem);
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + Cfg::OFF_BAR);  // [NS] TMA
     uint64_t* empty = full + NS;        // [NS] products done             (commit)
-    uint64_t* sc_full = empty + NS;     // [2] scaled                     (256)
+    uint64_t* sc_full = empty + NS;     // [2] scaled                     (8 warps)
     uint64_t* sc_free = sc_full + 2;    // [2] products done              (commit)
     uint64_t* acc_full = sc_full + 4;   // [2] a block's sum complete     (commit)
-    uint64_t* acc_free = sc_full + 6;   // [2] ... read                   (256)
-    uint64_t* w_full = sc_full + 8;     // [4] weights written            (32)
-    uint64_t* w_free = sc_full + 12;    // [4] ... read (256 scale, 256 update)
+    uint64_t* acc_free = sc_full + 6;   // [2] ... read                   (8 warps)
+    uint64_t* w_full = sc_full + 8;     // [4] weights written            (1)
+    uint64_t* w_free = sc_full + 12;    // [4] ... read (8 scale warps, 8 update warps)
     uint64_t* drain = sc_full + 16;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Cfg::OFF_MISC);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Cfg::OFF_MISC + 4);
@@ -97,14 +97,14 @@ gated_chain_kernel(const __grid_constant__ GatedChainParams prm) {
             mbar_init(&empty[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
-            mbar_init(&sc_full[b], 256);
+            mbar_init(&sc_full[b], 8);
             mbar_init(&sc_free[b], 1);
             mbar_init(&acc_full[b], 1);
-            mbar_init(&acc_free[b], 256);
+            mbar_init(&acc_free[b], 8);
         }
         for (int b = 0; b < 4; ++b) {
-            mbar_init(&w_full[b], 32);
-            mbar_init(&w_free[b], 512);
+            mbar_init(&w_full[b], 1);
+            mbar_init(&w_free[b], 16);
         }
         mbar_init(drain, 1);
         *abort_flag = 0;
@@ -217,7 +217,7 @@ gated_chain_kernel(const __grid_constant__ GatedChainParams prm) {
                 }
                 *reinterpret_cast<float4*>(wtab + (i & 3) * C + 4 * lane) = w;
                 if (lane == (REV ? 31 : 0)) tots[i & 3] = exp2f(sc);
-                mbar_arrive(&w_full[i & 3]);
+                warp_arrive(&w_full[i & 3]);
             }
         }
     } else if (warp >= 4 && warp < 12) {
@@ -226,25 +226,32 @@ gated_chain_kernel(const __grid_constant__ GatedChainParams prm) {
         constexpr int NV = EC / 16;  // 16-byte pieces
         // its pieces of B arrive by cp.async in a ring that only it reads
         uint4* ring = reinterpret_cast<uint4*>(smem + Cfg::OFF_B) + u;
-        int fi = 0, fg = 0;  // the block and head fetched next
-        uint32_t fn = 0;
+        // where the next piece is: its token, and steps to the next head and block
+        int fi = 0, fg = 0, fs = 0;
+        int64_t ft = int64_t(blk_of(0)) * C + row;
+        const int64_t head_step = prm.N * D;
+        const __nv_bfloat16* base = prm.b + int64_t(head) * ng * head_step + e0 + h * (EC / 2);
+        const __nv_bfloat16* fp = base + ft * D;
         auto fetch = [&]() {
             if (fi < steps) {
-                const int64_t t = int64_t(blk_of(fi)) * C + row;
-                const bool in = t < prm.N;
-                const uint4* src = reinterpret_cast<const uint4*>(
-                    prm.b + (int64_t(head * ng + fg) * prm.N + (in ? t : 0)) * D + e0 + h * (EC / 2));
+                const bool in = ft < prm.N;
+                const uint4* src = reinterpret_cast<const uint4*>(in ? fp : base);
 #pragma unroll
                 for (int j = 0; j < NV; ++j)
-                    copy16_async(ring + ((fn % Cfg::NB) * NV + j) * 256, src + j, in);
-                ++fn;
-                if (++fg == ng) {
+                    copy16_async(ring + (fs * NV + j) * 256, src + j, in);
+                fs = fs == Cfg::NB - 1 ? 0 : fs + 1;
+                if (++fg < ng) {
+                    fp += head_step;
+                } else {
                     fg = 0;
                     ++fi;
+                    ft += REV ? -C : C;
+                    fp += (REV ? -C : C) * D - (ng - 1) * head_step;
                 }
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
         };
+        int rs = 0;  // slot read next
         uint32_t n = 0;
         bool ok = true;
         for (int j = 0; j < Cfg::NB - 1; ++j) fetch();
@@ -256,7 +263,8 @@ gated_chain_kernel(const __grid_constant__ GatedChainParams prm) {
                 asm volatile("cp.async.wait_group %0;" ::"n"(Cfg::NB - 1) : "memory");
                 uint4 x[NV];
 #pragma unroll
-                for (int j = 0; j < NV; ++j) x[j] = ring[((n % Cfg::NB) * NV + j) * 256];
+                for (int j = 0; j < NV; ++j) x[j] = ring[(rs * NV + j) * 256];
+                rs = rs == Cfg::NB - 1 ? 0 : rs + 1;
                 if (!(ok = n < 2 || warp_wait(&sc_free[n & 1], ((n >> 1) - 1) & 1, abort_flag)))
                     break;
                 uint8_t* sc = smem + Cfg::OFF_SC + (n & 1) * Cfg::SC;
@@ -265,12 +273,10 @@ gated_chain_kernel(const __grid_constant__ GatedChainParams prm) {
                     uint32_t hi[4] = {x[j].x, x[j].y, x[j].z, x[j].w}, lo[4];
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
-                        float2 f = unpack_bf16(hi[c]);
-                        f.x *= w;
-                        f.y *= w;
+                        const float2 f = mul2(unpack_bf16(hi[c]), make_float2(w, w));
                         hi[c] = pack_bf16(f.x, f.y);
-                        const float2 r = unpack_bf16(hi[c]);
-                        lo[c] = pack_bf16(f.x - r.x, f.y - r.y);
+                        const float2 r = fma2(unpack_bf16(hi[c]), make_float2(-1.f, -1.f), f);
+                        lo[c] = pack_bf16(r.x, r.y);
                     }
                     const int q = h * NV + j;
                     *reinterpret_cast<uint4*>(sc + tile_chunk_off(C, row, q)) =
@@ -279,9 +285,9 @@ gated_chain_kernel(const __grid_constant__ GatedChainParams prm) {
                         make_uint4(lo[0], lo[1], lo[2], lo[3]);
                 }
                 fence_proxy_async_smem();
-                mbar_arrive(&sc_full[n & 1]);
+                warp_arrive(&sc_full[n & 1]);
             }
-            if (ok) mbar_arrive(&w_free[i & 3]);
+            if (ok) warp_arrive(&w_free[i & 3]);
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
     } else if (warp >= 12) {
@@ -326,8 +332,8 @@ gated_chain_kernel(const __grid_constant__ GatedChainParams prm) {
                 for (int c = 0; c < 16; ++c) run[j + c] = fmaf(a, run[j + c], hi[c] + lo[c]);
             }
             tc_fence_before();
-            mbar_arrive(&acc_free[i & 1]);
-            mbar_arrive(&w_free[i & 3]);
+            warp_arrive(&acc_free[i & 1]);
+            warp_arrive(&w_free[i & 3]);
         }
         if (ok) {
             if (prm.last) {

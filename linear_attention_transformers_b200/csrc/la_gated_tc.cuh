@@ -3,15 +3,16 @@
 //
 // The sequence is cut into blocks of C = 128 tokens and spans of L = 128 nb
 // tokens; states exist at the spans' borders only, and inside a span every
-// block meets the span's blocks before it (forward) or behind it (REV)
-// directly.  No block waits for another: all of the sequence is in flight at
+// block meets the span's blocks before it directly (the backward takes spans of
+// one block).  No block waits for another: all of the sequence is in flight at
 // once, whatever the number of heads, and the only serial step is the states'
-// recurrence over the spans (gated_border_kernel), which is elementwise.
+// recurrence over the spans, which is elementwise.
 //
 //   gated_span_kernel    a span's own part of the state, sum_t w_t A_t B_t^T
 //   gated_border_kernel  the recurrence; bf16 states entering every span
-//   gated_block_kernel   o, dq, dk or dv of a 128-token block
-//   gated_dgate_sum_kernel  dlog_gate from the pieces the blocks leave
+//   gated_chain_kernel   both, walking the sequence (la_gated_chain.cuh)
+//   gated_block_kernel   o of a 128-token block
+//   gated_bwd_kernel     dq, dk, dv and dlog_gate of one (la_gated_bwd.cuh)
 //
 // Bytes a token and head (D = 128, nb = 2): k and v once for the parts (4 D),
 // the records written, read and written again in bf16, and read (4 + 4 + 2 + 2
@@ -90,9 +91,41 @@ __device__ __forceinline__ uint32_t elect_lane() {
         : "=r"(one));
     return one;
 }
+// One arrival for a warp, after what each of its lanes did before (an arrival by
+// every thread is an operation on one shared word each: 512 of them, several
+// times a block, kept the shared-memory pipe busy for a third of the block).
+__device__ __forceinline__ void warp_arrive(uint64_t* bar) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) sm100::mbar_arrive(bar);
+}
 // All lanes wait; false for all when one of the waits gave up.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
     return __all_sync(0xffffffffu, sm100::mbar_wait(bar, parity, abort));
+}
+
+// Two float32 operations an instruction (each rounded as the single one is).
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 r;
+    asm("{\n\t.reg .b64 x, y, z;\n\t"
+        "mov.b64 x, {%2, %3};\n\t"
+        "mov.b64 y, {%4, %5};\n\t"
+        "mul.rn.f32x2 z, x, y;\n\t"
+        "mov.b64 {%0, %1}, z;\n\t}\n"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 r;
+    asm("{\n\t.reg .b64 x, y, z, w;\n\t"
+        "mov.b64 x, {%2, %3};\n\t"
+        "mov.b64 y, {%4, %5};\n\t"
+        "mov.b64 w, {%6, %7};\n\t"
+        "fma.rn.f32x2 z, x, y, w;\n\t"
+        "mov.b64 {%0, %1}, z;\n\t}\n"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return r;
 }
 
 __device__ __forceinline__ float ex2_fast(float x) {
@@ -177,13 +210,13 @@ gated_span_kernel(const __grid_constant__ GatedSpanParams prm) {
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sbase = smem_u32(smem);
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + Cfg::OFF_BAR);  // [NS] TMA
-    uint64_t* empty = full + NS;       // [NS] A: scaled (256); B: MMA done (commit)
-    uint64_t* sc_full = empty + NS;    // scaled operand written          (256)
+    uint64_t* empty = full + NS;       // [NS] A: scaled (8 warps); B: MMA done (commit)
+    uint64_t* sc_full = empty + NS;    // scaled operand written          (8 warps)
     uint64_t* sc_free = sc_full + 1;   // MMAs have read it               (commit)
     uint64_t* acc_full = sc_full + 2;  // [2] record complete             (commit)
-    uint64_t* acc_free = sc_full + 4;  // [2] record read                 (128)
-    uint64_t* w_full = sc_full + 6;    // [2] weights written             (32)
-    uint64_t* w_free = sc_full + 8;    // [2] weights read                (256)
+    uint64_t* acc_free = sc_full + 4;  // [2] record read                 (4 warps)
+    uint64_t* w_full = sc_full + 6;    // [2] weights written             (1)
+    uint64_t* w_free = sc_full + 8;    // [2] weights read                (8 warps)
     uint64_t* drain = sc_full + 10;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Cfg::OFF_MISC);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Cfg::OFF_MISC + 4);
@@ -193,15 +226,15 @@ gated_span_kernel(const __grid_constant__ GatedSpanParams prm) {
     if (tid == 0) {
         for (int s = 0; s < NS; ++s) {
             mbar_init(&full[s], 1);
-            mbar_init(&empty[s], (s & 1) ? 1 : 256);
+            mbar_init(&empty[s], (s & 1) ? 1 : 8);
         }
-        mbar_init(sc_full, 256);
+        mbar_init(sc_full, 8);
         mbar_init(sc_free, 1);
         for (int b = 0; b < 2; ++b) {
             mbar_init(&acc_full[b], 1);
-            mbar_init(&acc_free[b], 128);
-            mbar_init(&w_full[b], 32);
-            mbar_init(&w_free[b], 256);
+            mbar_init(&acc_free[b], 4);
+            mbar_init(&w_full[b], 1);
+            mbar_init(&w_free[b], 8);
         }
         mbar_init(drain, 1);
         *abort_flag = 0;
@@ -296,7 +329,7 @@ gated_span_kernel(const __grid_constant__ GatedSpanParams prm) {
                           total = all;
                       });
             if (lane == 0) prm.tot[head * prm.nspan + span] = exp2f(float(total));
-            mbar_arrive(&w_full[buf]);
+            warp_arrive(&w_full[buf]);
         }
     } else if (warp >= 4 && warp < 12) {
         // scale A's rows: thread u takes half a row (D / 2 elements)
@@ -321,7 +354,7 @@ gated_span_kernel(const __grid_constant__ GatedSpanParams prm) {
 #pragma unroll
                 for (int i = 0; i < D / 16; ++i)
                     x[i] = *reinterpret_cast<const uint4*>(src + tile_chunk_off(C, row, q0 + i));
-                mbar_arrive(&empty[s]);
+                warp_arrive(&empty[s]);
                 if (!(ok = __all_sync(0xffffffffu, blk == 0 || mbar_wait(sc_free, (blk - 1) & 1,
                                                                          abort_flag))))
                     break;
@@ -344,9 +377,9 @@ gated_span_kernel(const __grid_constant__ GatedSpanParams prm) {
                         make_uint4(l[0], l[1], l[2], l[3]);
                 }
                 fence_proxy_async_smem();
-                mbar_arrive(sc_full);
+                warp_arrive(sc_full);
             }
-            if (ok) mbar_arrive(&w_free[m & 1]);
+            if (ok) warp_arrive(&w_free[m & 1]);
         }
     } else if (warp >= 12) {
         const int sp = warp & 3;
@@ -370,7 +403,7 @@ gated_span_kernel(const __grid_constant__ GatedSpanParams prm) {
                 }
             }
             tc_fence_before();
-            mbar_arrive(&acc_free[m & 1]);
+            warp_arrive(&acc_free[m & 1]);
         }
     }
     tc_fence_before();
@@ -428,60 +461,49 @@ gated_border_kernel(const float4* __restrict__ rec, const float* __restrict__ to
         put(REV ? 0 : nspan - 1);
 }
 
-// ------------------------------------------------------------- o, dq, dk, dv
-// out_i = in_mul sum_j w_ij (R_i . K_j) V_j + st_mul r_i (R_i through the state)
-// (see gated_rows_kernel).  XTRA = 0: no more.  XTRA = 1: also the dot of a
-// second row tile with what came through the state, rowv_i = R2_i . st_mul r_i
-// (R_i S).  XTRA = 2: besides, M_ij = in_mul w_ij (R_i . K_j)(R2_i . V_j), its
-// sums over j < i added to rowv_i and its sums over the 32 rows of each
-// sub-block to colv.
+// -------------------------------------------------------------------------- o
+// o_i = scale sum_j e^{G_i-G_j} (q_i . k_j) v_j + scale e^{G_i} (q_i through S)
 struct GatedBlockParams {
-    CUtensorMap tm_row, tm_col, tm_val, tm_st, tm_out, tm_row2;
+    CUtensorMap tm_q, tm_k, tm_v, tm_st, tm_o;
     const __nv_bfloat16* lg;
-    float* rowv;      // [2][row heads][N]
-    float* colv;      // [row heads][4 nb][N]
-    int64_t N, items, heads;
+    int64_t N, items;
     int nblk, nb, nspan, group, has_state;
-    float in_mul, st_mul;
+    float scale;
 };
 
-template <int D, int XTRA>
+template <int D>
 struct GatedBlockCfg {
     static constexpr int TILE = kGtC * D * 2;
-    static constexpr int CTAS = D == 64 && XTRA < 2 ? 2 : 1;
-    // an item's row tiles stay for all of its column blocks, so they have
-    // buffers of their own (NR each) beside the ring of the others (NS)
-    static constexpr int NS = D == 64 && XTRA == 2 ? 8 : 4;
-    static constexpr int NR = XTRA == 0 || (D == 64 && XTRA == 2) ? 2 : 1;
-    static constexpr int ROWT = XTRA ? 2 : 1;                // row tiles of an item
-    static constexpr int NP = D == 128 && XTRA < 2 ? 2 : 1;  // P buffers
+    static constexpr int CTAS = D == 64 ? 2 : 1;
+    static constexpr int NS = 4;                     // ring of the k, v and state tiles
+    static constexpr int NR = 2;                     // q stays for all of its column blocks
+    static constexpr int NP = D == 128 ? 2 : 1;      // P buffers
+    static constexpr int NG = D == 128 ? 4 : 2;      // groups of four compute warps
+    static constexpr int THREADS = 128 + 128 * NG;
     static constexpr int OFF_ROW = NS * TILE;
-    static constexpr int OFF_TAB = OFF_ROW + NR * ROWT * TILE;
+    static constexpr int OFF_TAB = OFF_ROW + NR * TILE;
     static constexpr int OFF_BAR = OFF_TAB + 2 * int(sizeof(GateTab));
     static constexpr int NBAR = 2 * NS + 21;
     static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
     static constexpr int SMEM = OFF_MISC + 16 + 1024;
     static constexpr int T_P = 0;
-    static constexpr int T_P2 = kGtC;                        // XTRA = 2
-    static constexpr int T_ST = kGtC * (XTRA == 2 ? 2 : NP); // through the state
-    static constexpr int T_IN = T_ST + D;                    // inside the span
-    static constexpr int T_USED = T_IN + D;
-    static constexpr int T_COLS = T_USED <= 256 ? 256 : 512;
+    static constexpr int T_ST = kGtC * NP;           // through the state
+    static constexpr int T_IN = T_ST + D;            // inside the span
+    static constexpr int T_COLS = T_IN + D <= 256 ? 256 : 512;
     static_assert(CTAS * (SMEM + 1024) <= 228 * 1024, "shared memory budget");
     static_assert(CTAS * T_COLS <= 512, "TMEM budget");
 };
 
-// Warps: 0 TMA loads of the ring, 1 MMA, 2 gate tables and TMA loads of the
-// rows, 3 TMA stores, 4-11 compute: two groups of four warps, group h for the column half h of every C x C product
-// and of the output.
-constexpr int kGatedBlockThreads = 384;
-
-template <int D, bool REV, bool TRANS, int XTRA>
-__global__ void __launch_bounds__(kGatedBlockThreads, GatedBlockCfg<D, XTRA>::CTAS)
+// Warps: 0 TMA loads of the ring, 1 MMA, 2 gate tables and TMA loads of q, 3
+// TMA stores, from 4 on compute: NG groups of four warps, group h for 128 / NG
+// columns of every C x C product and D / NG of the output.
+template <int D>
+__global__ void __launch_bounds__(GatedBlockCfg<D>::THREADS, GatedBlockCfg<D>::CTAS)
 gated_block_kernel(const __grid_constant__ GatedBlockParams prm) {
     using namespace sm100;
-    using Cfg = GatedBlockCfg<D, XTRA>;
-    constexpr int C = kGtC, NS = Cfg::NS, NP = Cfg::NP;
+    using Cfg = GatedBlockCfg<D>;
+    constexpr int C = kGtC, NS = Cfg::NS, NP = Cfg::NP, NG = Cfg::NG;
+    constexpr int PW = C / NG;  // columns of P a group packs
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -489,16 +511,16 @@ gated_block_kernel(const __grid_constant__ GatedBlockParams prm) {
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + Cfg::OFF_BAR);  // [NS] TMA
     uint64_t* empty = full + NS;        // [NS] released (commit, or the store warp)
     uint64_t* p_full = empty + NS;      // [2] P complete                (commit)
-    uint64_t* pt_full = p_full + 2;     // [2] weighted P packed         (256)
+    uint64_t* pt_full = p_full + 2;     // [2] weighted P packed         (compute warps)
     uint64_t* p_free = p_full + 4;      // [2] ... consumed              (commit)
     uint64_t* o_full = p_full + 6;      // output accumulators complete  (commit)
-    uint64_t* o_free = p_full + 7;      // ... read                      (256)
-    uint64_t* out_full = p_full + 8;    // [2] output staged             (256)
+    uint64_t* o_free = p_full + 7;      // ... read                      (compute warps)
+    uint64_t* out_full = p_full + 8;    // [2] output staged             (compute warps)
     uint64_t* out_free = p_full + 10;   // [2] ... stored                (1)
-    uint64_t* tab_full = p_full + 12;   // [2] gate tables written       (32)
-    uint64_t* tab_free = p_full + 14;   // [2] ... read                  (256)
-    uint64_t* row_full = p_full + 16;   // [2] row tiles landed           (1 + tx)
-    uint64_t* row_free = p_full + 18;   // [2] ... read (commit; XTRA: and the epilogue)
+    uint64_t* tab_full = p_full + 12;   // [2] gate tables written       (1)
+    uint64_t* tab_free = p_full + 14;   // [2] ... read                  (compute warps)
+    uint64_t* row_full = p_full + 16;   // [2] q landed                  (1 + tx)
+    uint64_t* row_free = p_full + 18;   // [2] ... read                  (commit)
     uint64_t* drain = p_full + 20;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Cfg::OFF_MISC);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Cfg::OFF_MISC + 4);
@@ -512,19 +534,17 @@ gated_block_kernel(const __grid_constant__ GatedBlockParams prm) {
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&p_full[b], 1);
-            mbar_init(&pt_full[b], 256);
+            mbar_init(&pt_full[b], 4 * NG);
             mbar_init(&p_free[b], 1);
-            mbar_init(&out_full[b], 256);
+            mbar_init(&out_full[b], 4 * NG);
             mbar_init(&out_free[b], 1);
+            mbar_init(&tab_full[b], 1);
+            mbar_init(&tab_free[b], 4 * NG);
+            mbar_init(&row_full[b], 1);
+            mbar_init(&row_free[b], 1);
         }
         mbar_init(o_full, 1);
-        mbar_init(o_free, 256);
-        for (int b = 0; b < 2; ++b) {
-            mbar_init(&tab_full[b], 32);
-            mbar_init(&tab_free[b], 256);
-            mbar_init(&row_full[b], 1);
-            mbar_init(&row_free[b], XTRA ? 2 : 1);
-        }
+        mbar_init(o_free, 4 * NG);
         mbar_init(drain, 1);
         *abort_flag = 0;
         fence_mbar_init();
@@ -538,174 +558,147 @@ gated_block_kernel(const __grid_constant__ GatedBlockParams prm) {
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
 
-    // One item: 128 rows.  Its other tiles arrive in the ring in the order
-    // col 0, [state], val 0, col 1, val 1, ...
+    // One item: 128 rows of a query head.  Its other tiles arrive in the ring in
+    // the order k 0, [state], v 0, k 1, v 1, ...
     struct Item {
-        int64_t head, kvh;  // row head, key/value head
-        int span, rb;       // span of the head, block of the span
-        int nbv;            // blocks of this span
-        int per;            // column blocks a head
-        int ncb;            // column blocks (times the group's heads, REV)
-        int loads;          // tiles through the ring
+        int head, kvh;  // query head, key/value head
+        int span, rb;   // span of the head, block of the span
+        int ncb;        // column blocks: rb + 1
+        int loads;      // tiles through the ring
     };
     auto item_of = [&](int64_t it) {
         Item x;
         x.head = int(unsigned(it) / unsigned(prm.nblk));
         const int blk = int(unsigned(it) % unsigned(prm.nblk));
-        x.kvh = REV ? x.head : int(unsigned(x.head) / unsigned(prm.group));
+        x.kvh = int(unsigned(x.head) / unsigned(prm.group));
         x.span = blk / prm.nb;
-        x.nbv = min(prm.nb, prm.nblk - x.span * prm.nb);
+        const int nbv = min(prm.nb, prm.nblk - x.span * prm.nb);
         // the blocks of a span differ in cost by their place in it: turn the
         // order from span to span, so that a stride over the items (the grid)
         // meets every place
-        const unsigned s = unsigned(x.head * prm.nspan + x.span);
-        x.rb = int((unsigned(blk % prm.nb) + s + (s >> 1)) % unsigned(x.nbv));
-        x.per = REV ? x.nbv - x.rb : x.rb + 1;
-        x.ncb = REV ? x.per * prm.group : x.per;
+        const unsigned s = unsigned(x.head) * unsigned(prm.nspan) + unsigned(x.span);
+        x.rb = int((unsigned(blk % prm.nb) + s + (s >> 1)) % unsigned(nbv));
+        x.ncb = x.rb + 1;
         x.loads = (prm.has_state ? 1 : 0) + 2 * x.ncb;
         return x;
     };
-    // block of the span that column block b stands for
-    auto col_of = [&](const Item& x, int b) { return REV ? x.rb + b % x.per : b; };
 
     if (warp == 0) {
         if (lane == 0) {
-            tma_prefetch_desc(&prm.tm_col);
-            tma_prefetch_desc(&prm.tm_val);
+            tma_prefetch_desc(&prm.tm_k);
+            tma_prefetch_desc(&prm.tm_v);
             uint32_t n = 0;
             bool ok = true;
-            auto load = [&](const CUtensorMap* map, int rows, int row, int64_t head) {
+            auto load = [&](const CUtensorMap* map, int rows, int row, int head) {
                 const int s = n % NS;
                 if (n >= NS && !mbar_wait(&empty[s], ((n / NS) - 1) & 1, abort_flag)) return false;
                 mbar_arrive_expect_tx(&full[s], uint32_t(rows) * D * 2);
                 for (int a = 0; a < D / 64; ++a)
                     tma_load_3d(smem + s * Cfg::TILE + a * rows * 128, map, &full[s], 64 * a, row,
-                                int(head));
+                                head);
                 ++n;
                 return true;
             };
             for (int64_t it = blockIdx.x; ok && it < prm.items; it += gridDim.x) {
                 const Item x = item_of(it);
-                const int base = x.span * prm.nb;
                 for (int b = 0; ok && b < x.ncb; ++b) {
-                    const int64_t src = REV ? x.head * prm.group + b / x.per : x.kvh;
-                    const int row = (base + col_of(x, b)) * C;
-                    ok = load(&prm.tm_col, C, row, src);
+                    const int row = (x.span * prm.nb + b) * C;
+                    ok = load(&prm.tm_k, C, row, x.kvh);
                     if (ok && b == 0 && prm.has_state)
                         ok = load(&prm.tm_st, D, 0, x.kvh * prm.nspan + x.span);
-                    if (ok) ok = load(&prm.tm_val, C, row, src);
+                    if (ok) ok = load(&prm.tm_v, C, row, x.kvh);
                 }
             }
             for (uint32_t i = n > NS ? n - NS : 0; i < n; ++i)
                 mbar_wait_drain(&full[i % NS], (i / NS) & 1);
         }
     } else if (warp == 1) {
-        {
-            const uint32_t one = elect_lane();
-            constexpr uint32_t idP = idesc_bf16(C, C, 0, 0);             // rows x columns
-            constexpr uint32_t idS = idesc_bf16(C, D, 0, TRANS ? 0 : 1); // rows through S or S^T
-            constexpr uint32_t idV = idesc_bf16(C, D, 0, 1);             // weighted P, values
-            uint32_t n = 0, pc = 0, m = 0;
-            bool ok = true;
-            auto tile = [&](uint32_t i) { return sbase + (i % NS) * Cfg::TILE; };
-            auto landed = [&](uint32_t i) {
-                return warp_wait(&full[i % NS], (i / NS) & 1, abort_flag);
+        const uint32_t one = elect_lane();
+        constexpr uint32_t idP = idesc_bf16(C, C, 0, 0);  // rows x columns
+        constexpr uint32_t idV = idesc_bf16(C, D, 0, 1);  // rows through S; weighted P, values
+        uint32_t n = 0, pc = 0, m = 0;
+        bool ok = true;
+        auto tile = [&](uint32_t i) { return sbase + (i % NS) * Cfg::TILE; };
+        auto landed = [&](uint32_t i) {
+            return warp_wait(&full[i % NS], (i / NS) & 1, abort_flag);
+        };
+        for (int64_t it = blockIdx.x; ok && it < prm.items; it += gridDim.x, ++m) {
+            const Item x = item_of(it);
+            const uint32_t st = n + 1, hs = prm.has_state ? 1 : 0;
+            auto k_at = [&](int b) { return b == 0 ? n : n + hs + 2 * b; };
+            auto v_at = [&](int b) { return n + hs + 1 + 2 * b; };
+            const uint32_t rbuf = m % Cfg::NR;
+            const uint64_t dq = desc_k_base(sbase + Cfg::OFF_ROW + rbuf * Cfg::TILE);
+            // P of column block b, into the buffer that block b - NP is done with
+            auto p_part = [&](int b) {
+                const uint32_t i = pc + b, buf = i % NP;
+                if (i >= NP && !warp_wait(&p_free[buf], (i / NP - 1) & 1, abort_flag)) return false;
+                if (b == 0 && !warp_wait(&row_full[rbuf], (m / Cfg::NR) & 1, abort_flag))
+                    return false;
+                if (!landed(k_at(b))) return false;
+                tc_fence_after();
+                const uint64_t dk = desc_k_base(tile(k_at(b)));
+#pragma unroll
+                for (int k = 0; k < D; k += 16)
+                    umma_one(one, tmem + Cfg::T_P + buf * C, dq + kstep_k(C, k),
+                             dk + kstep_k(C, k), idP, k > 0);
+                commit_one(one, &p_full[buf]);
+                commit_one(one, &empty[k_at(b) % NS]);
+                return true;
             };
-            for (int64_t it = blockIdx.x; ok && it < prm.items; it += gridDim.x, ++m) {
-                const Item x = item_of(it);
-                const uint32_t st = n + 1, hs = prm.has_state ? 1 : 0;
-                auto col_at = [&](int b) { return b == 0 ? n : n + hs + 2 * b; };
-                auto val_at = [&](int b) { return n + hs + 1 + 2 * b; };
-                const uint32_t rbuf = m % Cfg::NR;
-                const uint32_t row = sbase + Cfg::OFF_ROW + rbuf * Cfg::ROWT * Cfg::TILE;
-                const uint64_t drow = desc_k_base(row);
-                // P of column block b, into the buffer that block b - NP is done with
-                auto p_part = [&](int b) {
-                    const uint32_t i = pc + b, buf = i % NP;
-                    if (i >= NP && !warp_wait(&p_free[buf], (i / NP - 1) & 1, abort_flag))
-                        return false;
-                    if (b == 0 && !warp_wait(&row_full[rbuf], (m / Cfg::NR) & 1, abort_flag))
-                        return false;
-                    if (!landed(col_at(b))) return false;
-                    if (XTRA == 2 && !landed(val_at(b))) return false;
-                    tc_fence_after();
-                    const uint64_t dcol = desc_k_base(tile(col_at(b)));
+            if (!(ok = p_part(0))) break;
+            if (m > 0 && !(ok = warp_wait(o_free, (m - 1) & 1, abort_flag))) break;
+            if (hs) {
+                if (!(ok = landed(st))) break;
+                tc_fence_after();
+                const uint64_t ds = desc_mn_base(tile(st), D);
 #pragma unroll
-                    for (int k = 0; k < D; k += 16)
-                        umma_one(one, tmem + Cfg::T_P + buf * C, drow + kstep_k(C, k),
-                                  dcol + kstep_k(C, k), idP, k > 0);
-                    if constexpr (XTRA == 2) {
-                        const uint64_t dr2 = desc_k_base(row + Cfg::TILE),
-                                       dv = desc_k_base(tile(val_at(b)));
-#pragma unroll
-                        for (int k = 0; k < D; k += 16)
-                            umma_one(one, tmem + Cfg::T_P2, dr2 + kstep_k(C, k), dv + kstep_k(C, k),
-                                      idP, k > 0);
-                    }
-                    commit_one(one, &p_full[buf]);
-                    commit_one(one, &empty[col_at(b) % NS]);
-                    return true;
-                };
-                if (!(ok = p_part(0))) break;
-                if (m > 0 && !(ok = warp_wait(o_free, (m - 1) & 1, abort_flag))) break;
-                if (hs) {
-                    if (!(ok = landed(st))) break;
-                    tc_fence_after();
-                    const uint64_t ds = TRANS ? desc_k_base(tile(st)) : desc_mn_base(tile(st), D);
-#pragma unroll
-                    for (int k = 0; k < D; k += 16)
-                        umma_one(one, tmem + Cfg::T_ST, drow + kstep_k(C, k),
-                                  ds + (TRANS ? kstep_k(D, k) : kstep_mn(k)), idS, k > 0);
-                    commit_one(one, &empty[st % NS]);
-                }
-                if (x.ncb == 1) commit_one(one, &row_free[rbuf]);
-                for (int b = 0; b < x.ncb; ++b) {
-                    if (NP == 2 && b + 1 < x.ncb) {
-                        if (!(ok = p_part(b + 1))) break;
-                        if (b + 2 == x.ncb) commit_one(one, &row_free[rbuf]);
-                    }
-                    const uint32_t i = pc + b;
-                    if (!(ok = warp_wait(&pt_full[i % NP], (i / NP) & 1, abort_flag))) break;
-                    if (!(ok = landed(val_at(b)))) break;
-                    tc_fence_after();
-                    const uint32_t tp = tmem + Cfg::T_P + (i % NP) * C;
-                    const uint64_t dv = desc_mn_base(tile(val_at(b)), C);
-                    // packed halves: columns 0.. and 64.. of the buffer
-#pragma unroll
-                    for (int k = 0; k < C; k += 16)
-                        umma_ts_one(one, tmem + Cfg::T_IN, tp + (k < 64 ? k / 2 : 32 + k / 2),
-                                     dv + kstep_mn(k), idV, b > 0 || k > 0);
-                    commit_one(one, &p_free[i % NP]);
-                    if (b + 1 < x.ncb)
-                        commit_one(one, &empty[val_at(b) % NS]);  // the last one: the store warp
-                    else
-                        commit_one(one, o_full);
-                    if (NP == 1 && b + 1 < x.ncb) {
-                        if (!(ok = p_part(b + 1))) break;
-                        if (b + 2 == x.ncb) commit_one(one, &row_free[rbuf]);
-                    }
-                }
-                pc += x.ncb;
-                n += x.loads;
+                for (int k = 0; k < D; k += 16)
+                    umma_one(one, tmem + Cfg::T_ST, dq + kstep_k(C, k), ds + kstep_mn(k), idV, k > 0);
+                commit_one(one, &empty[st % NS]);
             }
-            commit_one(one, drain);
-            if (lane == 0) mbar_wait_drain(drain, 0);
+            if (x.ncb == 1) commit_one(one, &row_free[rbuf]);
+            for (int b = 0; b < x.ncb; ++b) {
+                if (NP == 2 && b + 1 < x.ncb) {
+                    if (!(ok = p_part(b + 1))) break;
+                    if (b + 2 == x.ncb) commit_one(one, &row_free[rbuf]);
+                }
+                const uint32_t i = pc + b;
+                if (!(ok = warp_wait(&pt_full[i % NP], (i / NP) & 1, abort_flag))) break;
+                if (!(ok = landed(v_at(b)))) break;
+                tc_fence_after();
+                const uint32_t tp = tmem + Cfg::T_P + (i % NP) * C;
+                const uint64_t dv = desc_mn_base(tile(v_at(b)), C);
+                // a group packs its PW columns into the first half of them
+#pragma unroll
+                for (int k = 0; k < C; k += 16)
+                    umma_ts_one(one, tmem + Cfg::T_IN, tp + (k / PW) * PW + (k % PW) / 2,
+                                dv + kstep_mn(k), idV, b > 0 || k > 0);
+                commit_one(one, &p_free[i % NP]);
+                if (b + 1 < x.ncb)
+                    commit_one(one, &empty[v_at(b) % NS]);  // the last one: the store warp
+                else
+                    commit_one(one, o_full);
+                if (NP == 1 && b + 1 < x.ncb) {
+                    if (!(ok = p_part(b + 1))) break;
+                    if (b + 2 == x.ncb) commit_one(one, &row_free[rbuf]);
+                }
+            }
+            pc += x.ncb;
+            n += x.loads;
         }
+        commit_one(one, drain);
+        if (lane == 0) mbar_wait_drain(drain, 0);
     } else if (warp == 2) {
         uint32_t m = 0, issued = 0;
         auto load_rows = [&](const Item& x) {  // of item `issued`
             const uint32_t r = issued % Cfg::NR;
             if (lane == 0) {
-                uint8_t* dst = smem + Cfg::OFF_ROW + r * Cfg::ROWT * Cfg::TILE;
-                mbar_arrive_expect_tx(&row_full[r], Cfg::ROWT * Cfg::TILE);
-                const int row = (x.span * prm.nb + x.rb) * C;
-                for (int a = 0; a < D / 64; ++a) {
-                    tma_load_3d(dst + a * C * 128, &prm.tm_row, &row_full[r], 64 * a, row,
-                                int(x.head));
-                    if (XTRA)
-                        tma_load_3d(dst + Cfg::TILE + a * C * 128, &prm.tm_row2, &row_full[r],
-                                    64 * a, row, int(x.head));
-                }
+                uint8_t* dst = smem + Cfg::OFF_ROW + r * Cfg::TILE;
+                mbar_arrive_expect_tx(&row_full[r], Cfg::TILE);
+                for (int a = 0; a < D / 64; ++a)
+                    tma_load_3d(dst + a * C * 128, &prm.tm_q, &row_full[r], 64 * a,
+                                (x.span * prm.nb + x.rb) * C, x.head);
             }
             ++issued;
         };
@@ -713,20 +706,17 @@ gated_block_kernel(const __grid_constant__ GatedBlockParams prm) {
             const int buf = m & 1;
             const Item x = item_of(it);
             if (m < Cfg::NR) load_rows(x);
-            if (!__all_sync(0xffffffffu, m < 2 || mbar_wait(&tab_free[buf], ((m >> 1) - 1) & 1,
-                                                            abort_flag)))
-                break;
+            if (m >= 2 && !warp_wait(&tab_free[buf], ((m >> 1) - 1) & 1, abort_flag)) break;
             GateTab& tab = tabs[buf];
-            gate_sums(prm.lg + x.kvh * prm.N, int64_t(x.span) * prm.nb * C, prm.N, 4 * prm.nb,
-                      lane, tab.start, [&](int t, double run, double before, double end, double) {
+            gate_sums(prm.lg + int64_t(x.kvh) * prm.N, int64_t(x.span) * prm.nb * C, prm.N,
+                      4 * prm.nb, lane, tab.start,
+                      [&](int t, double run, double before, double end, double) {
                           tab.loc[t] = float(run - before);
-                          tab.fac[t] = ex2_fast(float(REV ? run - before : end - run));
+                          tab.fac[t] = ex2_fast(float(end - run));
                       });
-            mbar_arrive(&tab_full[buf]);
+            warp_arrive(&tab_full[buf]);
             if (m >= Cfg::NR) {
-                if (!__all_sync(0xffffffffu, mbar_wait(&row_free[m % Cfg::NR],
-                                                       (m / Cfg::NR - 1) & 1, abort_flag)))
-                    break;
+                if (!warp_wait(&row_free[m % Cfg::NR], (m / Cfg::NR - 1) & 1, abort_flag)) break;
                 load_rows(x);
             }
         }
@@ -742,19 +732,18 @@ gated_block_kernel(const __grid_constant__ GatedBlockParams prm) {
                 const uint32_t last = n + x.loads - 1;
                 const uint8_t* src = smem + (last % NS) * Cfg::TILE;
                 for (int a = 0; a < D / 64; ++a)
-                    tma_store_3d(&prm.tm_out, src + a * C * 128, 64 * a,
-                                 (x.span * prm.nb + x.rb) * C, int(x.head));
+                    tma_store_3d(&prm.tm_o, src + a * C * 128, 64 * a,
+                                 (x.span * prm.nb + x.rb) * C, x.head);
                 bulk_commit();
                 bulk_wait_read0();
                 mbar_arrive(&empty[last % NS]);
-                if (XTRA) mbar_arrive(&row_free[m % Cfg::NR]);  // the compute warps are done with it
                 mbar_arrive(&out_free[m & 1]);
                 n += x.loads;
             }
             bulk_wait0();
         }
     } else {
-        const int sp = warp & 3, half = (warp - 4) >> 2;
+        const int sp = warp & 3, grp = (warp - 4) >> 2;
         const uint32_t lane_base = uint32_t(32 * sp) << 16;
         const int irow = 32 * sp + lane;
         uint32_t n = 0, pc = 0, m = 0;
@@ -762,28 +751,20 @@ gated_block_kernel(const __grid_constant__ GatedBlockParams prm) {
         for (int64_t it = blockIdx.x; ok && it < prm.items; it += gridDim.x, ++m) {
             const Item x = item_of(it);
             const GateTab& tab = tabs[m & 1];
-            if (!(ok = __all_sync(0xffffffffu,
-                                  mbar_wait(&tab_full[m & 1], (m >> 1) & 1, abort_flag))))
-                break;
+            if (!(ok = warp_wait(&tab_full[m & 1], (m >> 1) & 1, abort_flag))) break;
             const int I = 4 * x.rb + sp;  // the warp's sub-block of rows
             const float gi = tab.loc[32 * I + lane];
             const double gI = tab.start[I];
-            const int64_t tok0 = int64_t(x.span * prm.nb + x.rb) * C;
-            float rsum = 0.f;
             for (int b = 0; b < x.ncb; ++b, ++pc) {
                 const int buf = pc % NP;
-                if (!(ok = __all_sync(0xffffffffu,
-                                      mbar_wait(&p_full[buf], (pc / NP) & 1, abort_flag))))
-                    break;
+                if (!(ok = warp_wait(&p_full[buf], (pc / NP) & 1, abort_flag))) break;
                 tc_fence_after();
-                const uint32_t reg = tmem + lane_base + Cfg::T_P + buf * C + 64 * half;
-                const int cb = col_of(x, b);
+                const uint32_t reg = tmem + lane_base + Cfg::T_P + buf * C + PW * grp;
 #pragma unroll 1
-                for (int s = 0; s < 2; ++s) {
-                    const int J = 4 * cb + 2 * half + s;  // sub-block of columns
+                for (int s = 0; s < PW / 32; ++s) {
+                    const int J = 4 * b + (PW / 32) * grp + s;  // sub-block of columns
                     float pv[32];
-                    const bool in = REV ? J >= I : J <= I;
-                    if (in) {
+                    if (J <= I) {
                         tmem_load<32>(reg + 32 * s, pv);
                         if (J == I) {
 #pragma unroll
@@ -791,15 +772,11 @@ gated_block_kernel(const __grid_constant__ GatedBlockParams prm) {
                                 const float4 g = *reinterpret_cast<const float4*>(&tab.loc[32 * J + t]);
                                 const float gj[4] = {g.x, g.y, g.z, g.w};
 #pragma unroll
-                                for (int w = 0; w < 4; ++w) {
-                                    const bool on = REV ? t + w >= lane : t + w <= lane;
-                                    pv[t + w] = on ? pv[t + w] * ex2_fast(REV ? gj[w] - gi : gi - gj[w])
-                                                   : 0.f;
-                                }
+                                for (int w = 0; w < 4; ++w)
+                                    pv[t + w] = t + w <= lane ? pv[t + w] * ex2_fast(gi - gj[w]) : 0.f;
                             }
                         } else {
-                            const float r = ex2_fast(REV ? float(tab.start[J] - gI) - gi
-                                                         : gi + float(gI - tab.start[J + 1]));
+                            const float r = ex2_fast(gi + float(gI - tab.start[J + 1]));
 #pragma unroll
                             for (int t = 0; t < 32; t += 4) {
                                 const float4 f = *reinterpret_cast<const float4*>(&tab.fac[32 * J + t]);
@@ -808,29 +785,6 @@ gated_block_kernel(const __grid_constant__ GatedBlockParams prm) {
                                 pv[t + 2] *= r * f.z;
                                 pv[t + 3] *= r * f.w;
                             }
-                        }
-                        if constexpr (XTRA == 2) {
-                            float p2[32];
-                            tmem_load<32>(tmem + lane_base + Cfg::T_P2 + 64 * half + 32 * s, p2);
-#pragma unroll
-                            for (int t = 0; t < 32; ++t) {
-                                // the diagonal itself passes no gate
-                                p2[t] *= J == I && t == lane ? 0.f : pv[t] * prm.in_mul;
-                                rsum += p2[t];
-                            }
-                            // column sums over the warp's rows: lane l ends with column l
-#pragma unroll
-                            for (int off = 16; off > 0; off >>= 1)
-#pragma unroll
-                                for (int t = 0; t < off; ++t) {
-                                    const bool up = (lane & off) != 0;
-                                    const float give = up ? p2[t] : p2[t + off];
-                                    const float keep = up ? p2[t + off] : p2[t];
-                                    p2[t] = keep + __shfl_xor_sync(0xffffffffu, give, off);
-                                }
-                            const int64_t tok = int64_t(x.span) * prm.nb * C + 32 * J + lane;
-                            if (tok < prm.N)
-                                prm.colv[(x.head * (4 * prm.nb) + I) * prm.N + tok] = p2[0];
                         }
                     } else {
 #pragma unroll
@@ -844,62 +798,34 @@ gated_block_kernel(const __grid_constant__ GatedBlockParams prm) {
                 }
                 tmem_wait_st();
                 tc_fence_before();
-                mbar_arrive(&pt_full[buf]);
+                warp_arrive(&pt_full[buf]);
             }
             if (!ok) break;
-            if (!(ok = __all_sync(0xffffffffu,
-                                  mbar_wait(o_full, m & 1, abort_flag) &&
-                                      (m < 2 || mbar_wait(&out_free[m & 1], ((m >> 1) - 1) & 1,
-                                                          abort_flag)))))
+            if (!(ok = warp_wait(o_full, m & 1, abort_flag) &&
+                       (m < 2 || warp_wait(&out_free[m & 1], ((m >> 1) - 1) & 1, abort_flag))))
                 break;
             tc_fence_after();
-            if (XTRA > 0 &&
-                !(ok = __all_sync(0xffffffffu, mbar_wait(&row_full[m % Cfg::NR],
-                                                         (m / Cfg::NR) & 1, abort_flag))))
-                break;
-            const float rr = prm.st_mul *
-                             ex2_fast(REV ? float(tab.start[4 * prm.nb] - gI) - gi : gi + float(gI));
+            const float rr = prm.scale * ex2_fast(gi + float(gI));
             uint8_t* ost = smem + ((n + x.loads - 1) % NS) * Cfg::TILE;
-            const uint8_t* row2 =
-                smem + Cfg::OFF_ROW + ((m % Cfg::NR) * Cfg::ROWT + Cfg::ROWT - 1) * Cfg::TILE;
 #pragma unroll 1
-            for (int c0 = half * (D / 2); c0 < (half + 1) * (D / 2); c0 += 32) {
+            for (int c0 = grp * (D / NG); c0 < (grp + 1) * (D / NG); c0 += 32) {
                 float ov[32];
                 tmem_load<32>(tmem + lane_base + Cfg::T_IN + c0, ov);
 #pragma unroll
-                for (int t = 0; t < 32; ++t) ov[t] *= prm.in_mul;
+                for (int t = 0; t < 32; ++t) ov[t] *= prm.scale;
                 if (prm.has_state) {
                     float sv[32];
                     tmem_load<32>(tmem + lane_base + Cfg::T_ST + c0, sv);
 #pragma unroll
-                    for (int t = 0; t < 32; ++t) {
-                        sv[t] *= rr;
-                        ov[t] += sv[t];
-                    }
-                    if constexpr (XTRA > 0) {
-#pragma unroll
-                        for (int t = 0; t < 32; t += 8) {
-                            const uint4 u = *reinterpret_cast<const uint4*>(
-                                row2 + tile_chunk_off(C, irow, (c0 + t) / 8));
-                            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                const float2 f = unpack_bf16(w[j]);
-                                rsum = fmaf(f.x, sv[t + 2 * j], rsum);
-                                rsum = fmaf(f.y, sv[t + 2 * j + 1], rsum);
-                            }
-                        }
-                    }
+                    for (int t = 0; t < 32; ++t) ov[t] = fmaf(rr, sv[t], ov[t]);
                 }
                 store_row_bf16<32>(ost, C, irow, c0, ov);
             }
-            if (XTRA > 0 && tok0 + irow < prm.N)
-                prm.rowv[(half * prm.heads + x.head) * prm.N + tok0 + irow] = rsum;
             fence_proxy_async_smem();
             tc_fence_before();
-            mbar_arrive(o_free);
-            mbar_arrive(&out_full[m & 1]);
-            mbar_arrive(&tab_free[m & 1]);
+            warp_arrive(o_free);
+            warp_arrive(&out_full[m & 1]);
+            warp_arrive(&tab_free[m & 1]);
             n += x.loads;
         }
     }
@@ -907,113 +833,6 @@ gated_block_kernel(const __grid_constant__ GatedBlockParams prm) {
     __syncthreads();
     tc_fence_after();
     if (warp == 1) tmem_dealloc(tmem, Cfg::T_COLS);
-}
-
-// ------------------------------------------------------------------ dlog_gate
-// One block a span and key/value head: sums over the group's heads of the row
-// values (rows' M sums and what came through S) less the column sums, from the
-// span's end on; of what passes through R, from its start on; and the product
-// of the two border states with all of the span's gates.
-struct GatedDgateParams {
-    const float* qrow;   // [2][B H][N]
-    const float* colv;   // [B H][4 nb][N]
-    const float* krow;   // [2][B Hkv][N], or null
-    const __nv_bfloat16* S;  // [kvh][nspan][D][D] or null
-    const __nv_bfloat16* R;
-    const __nv_bfloat16* lg;
-    __nv_bfloat16* dlg;
-    int64_t N, qheads, kvh;
-    int nspan, nb, nblk, group;
-};
-
-template <int D>
-__global__ void __launch_bounds__(256)
-gated_dgate_sum_kernel(const GatedDgateParams p) {
-    __shared__ float wsum[8];
-    __shared__ double gsum[8];
-    __shared__ float head_s[16], head_t[16];
-    const int64_t head = blockIdx.x / p.nspan;
-    const int span = int(blockIdx.x % p.nspan);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int64_t n0 = int64_t(span) * p.nb * kGtC;
-    const int nsub = 4 * min(p.nb, p.nblk - span * p.nb);
-    float x = 0.f;
-    if (p.S && p.R) {
-        const uint4* s4 = reinterpret_cast<const uint4*>(p.S + (head * p.nspan + span) * D * D);
-        const uint4* r4 = reinterpret_cast<const uint4*>(p.R + (head * p.nspan + span) * D * D);
-        for (int i = tid; i < D * D / 8; i += 256) {
-            const uint4 a = s4[i], b = r4[i];
-            const uint32_t u[4] = {a.x, a.y, a.z, a.w}, w[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float2 f = sm100::unpack_bf16(u[j]), g = sm100::unpack_bf16(w[j]);
-                x = fmaf(f.x, g.x, x);
-                x = fmaf(f.y, g.y, x);
-            }
-        }
-    }
-    x = warp_sum(x);
-    if (lane == 0) wsum[warp] = x;
-    double lsum = 0.0;  // the span's gates
-    for (int64_t n = n0 + tid; n < min(p.N, n0 + 32 * nsub); n += 256)
-        lsum += gate_log2(__bfloat162float(p.lg[head * p.N + n]));
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) lsum += __shfl_xor_sync(0xffffffffu, lsum, o);
-    if (lane == 0) gsum[warp] = lsum;
-    // sub-block J of warp J mod 8: d = rows less columns, t = through R, by lane
-    float d[2] = {0.f, 0.f}, t[2] = {0.f, 0.f};
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-        const int J = warp + 8 * u;
-        const int64_t n = n0 + 32 * J + lane;
-        if (J < nsub && n < p.N) {
-            for (int g = 0; g < p.group; ++g) {
-                const int64_t h = head * p.group + g;
-                d[u] += p.qrow[h * p.N + n] + p.qrow[(p.qheads + h) * p.N + n];
-                for (int I = J; I < nsub; ++I)
-                    d[u] -= p.colv[(h * (4 * p.nb) + I) * p.N + n];
-            }
-            if (p.krow) t[u] = p.krow[head * p.N + n] + p.krow[(p.kvh + head) * p.N + n];
-        }
-    }
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-        const float a = warp_sum(d[u]), b = warp_sum(t[u]);
-        if (lane == 0) {
-            head_s[warp + 8 * u] = a;
-            head_t[warp + 8 * u] = b;
-        }
-    }
-    __syncthreads();
-    float all = 0.f;
-    double gall = 0.0;
-#pragma unroll
-    for (int w = 0; w < 8; ++w) {
-        all += wsum[w];
-        gall += gsum[w];
-    }
-    all *= exp2f(float(gall));
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-        const int J = warp + 8 * u;
-        if (J >= nsub) continue;
-        float s = d[u], q = t[u];
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const float a = __shfl_down_sync(0xffffffffu, s, o);
-            const float b = __shfl_up_sync(0xffffffffu, q, o);
-            if (lane + o < 32) s += a;
-            if (lane >= o) q += b;
-        }
-        // before the token: shifted, not subtracted, since a token's own term may
-        // be larger than all before it by more than float32 holds
-        q = __shfl_up_sync(0xffffffffu, q, 1);
-        if (lane == 0) q = 0.f;
-        for (int w = J + 1; w < nsub; ++w) s += head_s[w];
-        for (int w = 0; w < J; ++w) q += head_t[w];
-        const int64_t n = n0 + 32 * J + lane;
-        if (n < p.N) p.dlg[head * p.N + n] = __float2bfloat16_rn(s + q + all);
-    }
 }
 
 }  // namespace la
