@@ -104,13 +104,13 @@ GatedTcPlan plan_gated_tc(la_op op, int64_t B, int64_t H, int64_t Hkv, int64_t N
 template <typename T, int D>
 constexpr bool gated_on_tensor_cores = std::is_same<T, __nv_bfloat16>::value && (D == 64 || D == 128);
 
-// Sizes a gated launch can take: one block per 64 tokens of a head.
+// Sizes a gated launch can take: at most four blocks per 64 tokens of a head.
 la_status check_gated(int64_t B, int64_t H, int64_t Hkv, int64_t N, int64_t D, la_dtype dt) {
     la_status s;
     if (dt != LA_F32 && dt != LA_BF16) return LA_ERR_INVALID_ARG;
     if ((s = check_sizes(B, H, N, D)) != LA_OK) return s;
     if ((s = check_group(H, Hkv)) != LA_OK) return s;
-    if (N > 0 && B * H > kMaxBlocks / ((N + la::kGatedC - 1) / la::kGatedC))
+    if (N > 0 && 4 * B * H > kMaxBlocks / ((N + la::kGatedC - 1) / la::kGatedC))
         return LA_ERR_UNSUPPORTED;
     return LA_OK;
 }
@@ -134,43 +134,38 @@ la_status allow_smem(K kern, size_t bytes) {
 }
 
 // ------------------------------------------------------ the plain-core kernels
-// Border states of every chunk: parts, then the recurrence.  `last` (may be
-// null) receives the state after the last chunk walked.
-template <typename T, int D, bool REV>
-la_status gated_states(const T* A, const T* Bm, const T* lg, float* rec, float* tot,
-                       const float* first, float* last, int64_t kvh, int64_t N, int64_t nchunk,
-                       int group, float mul, cudaStream_t st) {
+// Border states of every chunk: parts, then the recurrence; the forward
+// direction (S, from k and v) and the backward one (R, from q and dO) together.
+// A job without records is left out; `last` (may be null) receives the state
+// after the last chunk walked.
+template <typename T, int D>
+la_status gated_states(la::GatedPartJob f, la::GatedCarryJob fc, la::GatedPartJob r,
+                       la::GatedCarryJob rc, const T* lg, int64_t kvh, int64_t N, int64_t nchunk,
+                       cudaStream_t st) {
     la_status s;
-    const int run = int(last ? nchunk : nchunk - 1);
-    if (run > 0) {
+    auto fill = [&](la::GatedPartJob& p, la::GatedCarryJob& c, bool rev) {
+        p.run = int(!c.rec ? 0 : c.last ? nchunk : nchunk - 1);
+        p.chunk0 = rev && !c.last ? 1 : 0;
+        p.blocks = kvh * p.run;
+        p.rec = reinterpret_cast<float*>(c.rec);
+        p.gtot = const_cast<float*>(c.gtot);
+    };
+    fill(f, fc, false);
+    fill(r, rc, true);
+    if (f.blocks + r.blocks > 0) {
         const size_t smem = size_t(2) * la::kGatedC * la::GatedTile::ld(D) * 4;
-        auto kern = la::gated_part_kernel<T, D, REV>;
+        auto kern = la::gated_part_kernel<T, D>;
         if ((s = allow_smem(kern, smem)) != LA_OK) return s;
-        la::LaunchScope scope(REV ? "gated_part_rev" : "gated_part", st);
-        kern<<<unsigned(kvh * run), la::kGatedThreads, smem, st>>>(
-            A, Bm, lg, rec, tot, N, int(nchunk), run, REV && !last ? 1 : 0, group, mul);
+        la::LaunchScope scope("gated_part", st);
+        kern<<<unsigned(f.blocks + r.blocks), la::kGatedThreads, smem, st>>>(f, r, lg, N,
+                                                                            int(nchunk));
+        if ((s = launch_status()) != LA_OK) return s;
     }
     const int per = D * D / 4;
     const int64_t total = kvh * per;
-    la::LaunchScope scope(REV ? "gated_carry_rev" : "gated_carry", st);
-    la::gated_carry_kernel<REV><<<unsigned((total + 127) / 128), 128, 0, st>>>(
-        reinterpret_cast<float4*>(rec), tot, reinterpret_cast<const float4*>(first),
-        reinterpret_cast<float4*>(last), total, per, int(nchunk));
-    return launch_status();
-}
-
-template <typename T, int D, bool REV, bool TRANS>
-la_status gated_rows(const char* name, const T* R, const T* K, const T* V, const T* lg,
-                     const float* rec, T* out, int64_t heads, int64_t N, int64_t nchunk,
-                     int group, float in_mul, float st_mul, cudaStream_t st) {
-    la_status s;
-    const size_t smem = (size_t(3) * la::kGatedC * la::GatedTile::ld(D) +
-                         la::kGatedC * la::GatedTile::ld(la::kGatedC)) * 4;
-    auto kern = la::gated_rows_kernel<T, D, REV, TRANS>;
-    if ((s = allow_smem(kern, smem)) != LA_OK) return s;
-    la::LaunchScope scope(name, st);
-    kern<<<unsigned(heads * nchunk), la::kGatedThreads, smem, st>>>(
-        R, K, V, lg, rec, out, N, int(nchunk), group, in_mul, st_mul);
+    la::LaunchScope scope("gated_carry", st);
+    la::gated_carry_kernel<<<dim3(unsigned((total + 127) / 128), rc.rec ? 2 : 1), 128, 0, st>>>(
+        fc, rc, total, per, int(nchunk));
     return launch_status();
 }
 
@@ -319,21 +314,29 @@ template <typename T, int D>
 la_status run_gated_fwd(const void* q, const void* k, const void* v, const void* lg, void* o,
                         const float* S_in, float* S_out, float scale, int64_t B, int64_t H,
                         int64_t Hkv, int64_t N, char* ws, cudaStream_t st) {
+    la_status s;
     const GatedPlan p = plan_gated(LA_OP_FORWARD, B, Hkv, N, D);
-    const int group = int(H / Hkv);
-    const T *tq = static_cast<const T*>(q), *tk = static_cast<const T*>(k),
-            *tv = static_cast<const T*>(v), *tl = static_cast<const T*>(lg);
-    float* rec = reinterpret_cast<float*>(ws + p.s_rec);
-    const bool through = p.nchunk > 1 || S_in || S_out;
-    if (through) {
-        la_status s = gated_states<T, D, false>(tk, tv, tl, rec,
-                                                reinterpret_cast<float*>(ws + p.s_tot), S_in,
-                                                S_out, B * Hkv, N, p.nchunk, 1, 1.f, st);
-        if (s != LA_OK) return s;
+    la::GatedTensors<T> t{};
+    t.q = static_cast<const T*>(q), t.k = static_cast<const T*>(k), t.v = static_cast<const T*>(v);
+    t.lg = static_cast<const T*>(lg), t.o = static_cast<T*>(o);
+    t.N = N, t.qheads = B * H, t.kvh = B * Hkv, t.nchunk = int(p.nchunk);
+    t.group = int(H / Hkv), t.scale = scale;
+    if (p.nchunk > 1 || S_in || S_out) {
+        t.S = reinterpret_cast<float*>(ws + p.s_rec);
+        const la::GatedPartJob f{k, v, nullptr, nullptr, 0, 0, 0, 1, 1.f};
+        const la::GatedCarryJob fc{reinterpret_cast<float4*>(ws + p.s_rec),
+                                   reinterpret_cast<float*>(ws + p.s_tot),
+                                   reinterpret_cast<const float4*>(S_in),
+                                   reinterpret_cast<float4*>(S_out)};
+        if ((s = gated_states<T, D>(f, fc, {}, {}, t.lg, t.kvh, N, p.nchunk, st)) != LA_OK) return s;
     }
-    return gated_rows<T, D, false, false>("gated_o", tq, tk, tv, tl, through ? rec : nullptr,
-                                          static_cast<T*>(o), B * H, N, p.nchunk, group, scale,
-                                          scale, st);
+    const size_t smem = (size_t(3) * la::kGatedC * la::GatedTile::ld(D) +
+                         la::kGatedC * la::GatedTile::ld(la::kGatedC)) * 4;
+    auto kern = la::gated_o_kernel<T, D>;
+    if ((s = allow_smem(kern, smem)) != LA_OK) return s;
+    la::LaunchScope scope("gated_o", st);
+    kern<<<unsigned(t.qheads * p.nchunk), la::kGatedThreads, smem, st>>>(t);
+    return launch_status();
 }
 
 template <typename T, int D>
@@ -343,40 +346,36 @@ la_status run_gated_bwd(const void* q, const void* k, const void* v, const void*
                         int64_t H, int64_t Hkv, int64_t N, char* ws, cudaStream_t st) {
     la_status s;
     const GatedPlan p = plan_gated(LA_OP_BACKWARD, B, Hkv, N, D);
-    const int group = int(H / Hkv);
-    const int64_t kvh = B * Hkv;
-    const T *tq = static_cast<const T*>(q), *tk = static_cast<const T*>(k),
-            *tv = static_cast<const T*>(v), *tl = static_cast<const T*>(lg),
-            *td = static_cast<const T*>(dO);
-    float *S = nullptr, *R = nullptr;
+    la::GatedTensors<T> t{};
+    t.q = static_cast<const T*>(q), t.k = static_cast<const T*>(k), t.v = static_cast<const T*>(v);
+    t.lg = static_cast<const T*>(lg), t.dO = static_cast<const T*>(dO);
+    t.dq = static_cast<T*>(dq), t.dk = static_cast<T*>(dk), t.dv = static_cast<T*>(dv);
+    t.dlg = static_cast<T*>(dlg);
+    t.N = N, t.qheads = B * H, t.kvh = B * Hkv, t.nchunk = int(p.nchunk);
+    t.group = int(H / Hkv), t.scale = scale;
+    la::GatedCarryJob fc{}, rc{};
     if (p.nchunk > 1 || S_in) {
-        S = reinterpret_cast<float*>(ws + p.s_rec);
-        if ((s = gated_states<T, D, false>(tk, tv, tl, S, reinterpret_cast<float*>(ws + p.s_tot),
-                                           S_in, nullptr, kvh, N, p.nchunk, 1, 1.f, st)) != LA_OK)
-            return s;
+        t.S = reinterpret_cast<float*>(ws + p.s_rec);
+        fc = {reinterpret_cast<float4*>(ws + p.s_rec), reinterpret_cast<float*>(ws + p.s_tot),
+              reinterpret_cast<const float4*>(S_in), nullptr};
     }
     if (p.nchunk > 1 || dS_out || dS_in) {
-        R = reinterpret_cast<float*>(ws + p.r_rec);
-        if ((s = gated_states<T, D, true>(tq, td, tl, R, reinterpret_cast<float*>(ws + p.r_tot),
-                                          dS_out, dS_in, kvh, N, p.nchunk, group, scale, st)) !=
-            LA_OK)
-            return s;
+        t.R = reinterpret_cast<float*>(ws + p.r_rec);
+        rc = {reinterpret_cast<float4*>(ws + p.r_rec), reinterpret_cast<float*>(ws + p.r_tot),
+              reinterpret_cast<const float4*>(dS_out), reinterpret_cast<float4*>(dS_in)};
     }
-    if ((s = gated_rows<T, D, false, true>("gated_dq", td, tv, tk, tl, S, static_cast<T*>(dq),
-                                           B * H, N, p.nchunk, group, scale, scale, st)) != LA_OK)
-        return s;
-    if ((s = gated_rows<T, D, true, true>("gated_dk", tv, td, tq, tl, R, static_cast<T*>(dk), kvh,
-                                          N, p.nchunk, group, scale, 1.f, st)) != LA_OK)
-        return s;
-    if ((s = gated_rows<T, D, true, false>("gated_dv", tk, tq, td, tl, R, static_cast<T*>(dv),
-                                           kvh, N, p.nchunk, group, scale, 1.f, st)) != LA_OK)
-        return s;
-    const size_t smem = size_t(4) * la::kGatedC * la::GatedTile::ld(D) * 4;
-    auto kern = la::gated_dgate_kernel<T, D>;
+    if (t.S || t.R) {
+        const la::GatedPartJob f{k, v, nullptr, nullptr, 0, 0, 0, 1, 1.f};
+        const la::GatedPartJob r{q, dO, nullptr, nullptr, 0, 0, 0, t.group, scale};
+        if ((s = gated_states<T, D>(f, fc, r, rc, t.lg, t.kvh, N, p.nchunk, st)) != LA_OK) return s;
+    }
+    // dlog_gate's four tiles, or three and the C x C product
+    const size_t smem = (size_t(3) * la::kGatedC * la::GatedTile::ld(D) +
+                         la::kGatedC * la::GatedTile::ld(std::max(D, la::kGatedC))) * 4;
+    auto kern = la::gated_grad_kernel<T, D>;
     if ((s = allow_smem(kern, smem)) != LA_OK) return s;
-    la::LaunchScope scope("gated_dgate", st);
-    kern<<<unsigned(kvh * p.nchunk), la::kGatedThreads, smem, st>>>(
-        tq, tk, tv, td, tl, S, R, static_cast<T*>(dlg), N, int(p.nchunk), group, scale);
+    la::LaunchScope scope("gated_grad", st);
+    kern<<<unsigned((3 * t.kvh + t.qheads) * p.nchunk), la::kGatedThreads, smem, st>>>(t);
     return launch_status();
 }
 

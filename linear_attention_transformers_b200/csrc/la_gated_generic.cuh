@@ -4,10 +4,15 @@
 // every head a block of its own; the states at the chunks' borders are float32
 // records in the workspace:
 //
-//   gated_part_kernel   one chunk's own part of the state
+//   gated_part_kernel   the chunks' own parts of the state, both directions
 //   gated_carry_kernel  the records' recurrence over the chunks, in place
-//   gated_rows_kernel   o, dq, dk or dv of one chunk
-//   gated_dgate_kernel  dlog_gate of one chunk
+//   gated_o_kernel      o of one chunk
+//   gated_grad_kernel   dlog_gate, dk, dv and dq: each of a chunk a block's work
+//
+// What does not depend on each other shares a launch (the backward's four
+// gradients, the two directions of the states), since the sizes that come here
+// leave most SMs idle: B2 H6 Hkv2 N333 D64 float32, backward, 132 us in eight
+// launches.
 //
 // All products are register-tiled float32 (4 rows x D/16 columns a thread)
 // from float32 tiles in shared memory, so nothing is rounded below float32;
@@ -120,22 +125,32 @@ __device__ __forceinline__ void gated_mm_nn(float (&acc)[4][NC], const float* X,
 // rec[head][chunk] = sum over the chunk (and the G query heads of a group for
 // REV) of w_t A_t B_t^T: forward w_t = e^{G_C - G_t}, REV w_t = mul e^{G_t}.
 // gtot[head][chunk] = e^{G_C}.
+struct GatedPartJob {
+    const void *A, *B;
+    float *rec, *gtot;
+    int64_t blocks;             // heads * run; 0: nothing to do
+    int run, chunk0, group;     // chunks that are run, from chunk0 on
+    float mul;
+};
+
 template <typename T, int D, bool REV>
-__global__ void __launch_bounds__(kGatedThreads)
-gated_part_kernel(const T* __restrict__ A, const T* __restrict__ B, const T* __restrict__ lg,
-                  float* __restrict__ rec, float* __restrict__ gtot, int64_t N, int nchunk,
-                  int chunks_run, int chunk0, int group, float mul) {
+__device__ __forceinline__ void gated_part_block(const GatedPartJob& job, const T* __restrict__ lg,
+                                                 int64_t N, int nchunk, int64_t block) {
     constexpr int LD = GatedTile::ld(D);
     extern __shared__ __align__(16) float sm[];
     float* ta = sm;
     float* tb = sm + kGatedC * LD;
     __shared__ double G[kGatedC];
-    const int64_t head = blockIdx.x / chunks_run;
-    const int chunk = chunk0 + int(blockIdx.x % chunks_run);
+    const T* A = static_cast<const T*>(job.A);
+    const T* B = static_cast<const T*>(job.B);
+    const int group = job.group;
+    const float mul = job.mul;
+    const int64_t head = block / job.run;
+    const int chunk = job.chunk0 + int(block % job.run);
     const int64_t n0 = int64_t(chunk) * kGatedC;
     gated_load_gates(G, lg + head * N, n0, N);
     __syncthreads();
-    if (threadIdx.x == 0) gtot[head * nchunk + chunk] = exp2f(float(G[kGatedC - 1]));
+    if (threadIdx.x == 0) job.gtot[head * nchunk + chunk] = exp2f(float(G[kGatedC - 1]));
     // rows of the record: RD = max(1, D/16) a thread, columns tx + 16 c
     constexpr int NC = D / 16, NR = D / 16;
     const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
@@ -165,11 +180,22 @@ gated_part_kernel(const T* __restrict__ A, const T* __restrict__ B, const T* __r
                 for (int c = 0; c < NC; ++c) acc[r][c] = fmaf(x[r], y[c], acc[r][c]);
         }
     }
-    float* out = rec + (head * nchunk + chunk) * int64_t(D) * D;
+    float* out = job.rec + (head * nchunk + chunk) * int64_t(D) * D;
 #pragma unroll
     for (int r = 0; r < NR; ++r)
 #pragma unroll
         for (int c = 0; c < NC; ++c) out[(ty + 16 * r) * D + tx + 16 * c] = acc[r][c];
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kGatedThreads)
+gated_part_kernel(const GatedPartJob fwd, const GatedPartJob rev, const T* __restrict__ lg,
+                  int64_t N, int nchunk) {
+    const int64_t b = blockIdx.x;
+    if (b < rev.blocks)  // the longer ones (group heads each) first
+        gated_part_block<T, D, true>(rev, lg, N, nchunk, b);
+    else
+        gated_part_block<T, D, false>(fwd, lg, N, nchunk, b - rev.blocks);
 }
 
 // ------------------------------------------------------- the chunks' recurrence
@@ -178,13 +204,20 @@ gated_part_kernel(const T* __restrict__ A, const T* __restrict__ B, const T* __r
 // be null; then the part of the chunk walked last is neither computed nor
 // read).  One float4 of the state a thread; the next records are loaded while
 // the recurrence runs.
+struct GatedCarryJob {
+    float4* rec;
+    const float* gtot;
+    const float4* first;
+    float4* last;
+};
+
 template <bool REV>
-__global__ void __launch_bounds__(128)
-gated_carry_kernel(float4* __restrict__ rec, const float* __restrict__ gtot,
-                   const float4* __restrict__ first, float4* __restrict__ last, int64_t total,
-                   int per_head, int nchunk) {
-    const int64_t i = int64_t(blockIdx.x) * blockDim.x + threadIdx.x;
-    if (i >= total) return;
+__device__ __forceinline__ void gated_carry(const GatedCarryJob& job, int64_t i, int per_head,
+                                            int nchunk) {
+    float4* __restrict__ rec = job.rec;
+    const float* __restrict__ gtot = job.gtot;
+    const float4* __restrict__ first = job.first;
+    float4* __restrict__ last = job.last;
     const int64_t head = i / per_head, e = i % per_head;
     float4* r = rec + head * nchunk * per_head + e;
     const float* gt = gtot + head * nchunk;
@@ -219,6 +252,20 @@ gated_carry_kernel(float4* __restrict__ rec, const float* __restrict__ gtot,
         r[int64_t(REV ? 0 : nchunk - 1) * per_head] = run;
 }
 
+// blockIdx.y: 0 the first job, forwards; 1 the second, backwards; a job without
+// records is skipped
+__global__ void __launch_bounds__(128)
+gated_carry_kernel(const GatedCarryJob fwd, const GatedCarryJob rev, int64_t total, int per_head,
+                   int nchunk) {
+    const int64_t i = int64_t(blockIdx.x) * blockDim.x + threadIdx.x;
+    if (i >= total) return;
+    if (blockIdx.y == 0) {
+        if (fwd.rec) gated_carry<false>(fwd, i, per_head, nchunk);
+    } else {
+        if (rev.rec) gated_carry<true>(rev, i, per_head, nchunk);
+    }
+}
+
 // acc[r][c] += sum_e X[row r][e] Y[e][col c] with Y the record S (TRANS false,
 // Y[e][c] = S[e][c]) or its transpose (Y[e][c] = S[c][e]), 64 rows of Y at a
 // time through the shared tile `buf` ([64][D + 4] floats).
@@ -251,10 +298,10 @@ __device__ __forceinline__ void gated_mm_state(float (&acc)[4][D / 16], const fl
 // e^{G_j-G_i}, r = e^{G_C-G_i}; row heads are key/value heads and the columns
 // run over the group's query heads.  TRANS: rows meet S^T (dq, dk).
 template <typename T, int D, bool REV, bool TRANS>
-__global__ void __launch_bounds__(kGatedThreads)
-gated_rows_kernel(const T* __restrict__ R, const T* __restrict__ K, const T* __restrict__ V,
-                  const T* __restrict__ lg, const float* __restrict__ rec, T* __restrict__ out,
-                  int64_t N, int nchunk, int group, float in_mul, float st_mul) {
+__device__ __forceinline__ void gated_rows_block(
+    const T* __restrict__ R, const T* __restrict__ K, const T* __restrict__ V,
+    const T* __restrict__ lg, const float* __restrict__ rec, T* __restrict__ out, int64_t N,
+    int nchunk, int group, float in_mul, float st_mul, int64_t block) {
     constexpr int LD = GatedTile::ld(D), LP = GatedTile::ld(kGatedC), NC = D / 16;
     extern __shared__ __align__(16) float sm[];
     float* tr = sm;
@@ -262,8 +309,8 @@ gated_rows_kernel(const T* __restrict__ R, const T* __restrict__ K, const T* __r
     float* tv = tk + kGatedC * LD;
     float* tp = tv + kGatedC * LD;
     __shared__ double G[kGatedC];
-    const int64_t head = blockIdx.x / nchunk;
-    const int chunk = int(blockIdx.x % nchunk);
+    const int64_t head = block / nchunk;
+    const int chunk = int(block % nchunk);
     const int64_t kvh = REV ? head : head / group;
     const int64_t n0 = int64_t(chunk) * kGatedC;
     const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
@@ -314,11 +361,11 @@ gated_rows_kernel(const T* __restrict__ R, const T* __restrict__ K, const T* __r
 
 // ------------------------------------------------------------------ dlog_gate
 template <typename T, int D>
-__global__ void __launch_bounds__(kGatedThreads)
-gated_dgate_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v,
-                   const T* __restrict__ dO, const T* __restrict__ lg,
-                   const float* __restrict__ recS, const float* __restrict__ recR,
-                   T* __restrict__ dlg, int64_t N, int nchunk, int group, float scale) {
+__device__ __forceinline__ void gated_dgate_block(
+    const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v,
+    const T* __restrict__ dO, const T* __restrict__ lg, const float* __restrict__ recS,
+    const float* __restrict__ recR, T* __restrict__ dlg, int64_t N, int nchunk, int group,
+    float scale, int64_t block) {
     constexpr int LD = GatedTile::ld(D), NC = D / 16;
     extern __shared__ __align__(16) float sm[];
     float* ta = sm;                     // q, then k
@@ -330,8 +377,8 @@ gated_dgate_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __
     __shared__ float cols[16][kGatedC];       // sum_i M_ij (i > j), by j, one row a ty
     __shared__ float through[kGatedC];        // k_j.dk^R_j
     __shared__ float wsum[kGatedThreads / 32];
-    const int64_t head = blockIdx.x / nchunk;
-    const int chunk = int(blockIdx.x % nchunk);
+    const int64_t head = block / nchunk;
+    const int chunk = int(block % nchunk);
     const int64_t n0 = int64_t(chunk) * kGatedC;
     const int tid = threadIdx.x, ty = tid / 16, tx = tid % 16;
     const float* S = recS ? recS + (head * nchunk + chunk) * int64_t(D) * D : nullptr;
@@ -440,6 +487,43 @@ gated_dgate_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __
         const int64_t n = n0 + 2 * tid;
         if (n < N) dlg[head * N + n] = from_f32<T>(s + before + all);
         if (n + 1 < N) dlg[head * N + n + 1] = from_f32<T>(d1 + behind + (before + t0) + all);
+    }
+}
+
+// -------------------------------------------------------------------- launches
+template <typename T>
+struct GatedTensors {
+    const T *q, *k, *v, *lg, *dO;
+    T *o, *dq, *dk, *dv, *dlg;
+    const float *S, *R;         // records, or null
+    int64_t N, qheads, kvh;
+    int nchunk, group;
+    float scale;
+};
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kGatedThreads) gated_o_kernel(const GatedTensors<T> p) {
+    gated_rows_block<T, D, false, false>(p.q, p.k, p.v, p.lg, p.S, p.o, p.N, p.nchunk, p.group,
+                                         p.scale, p.scale, blockIdx.x);
+}
+
+// A block a chunk and gradient; the longest work first.
+template <typename T, int D>
+__global__ void __launch_bounds__(kGatedThreads) gated_grad_kernel(const GatedTensors<T> p) {
+    const int64_t kvb = p.kvh * p.nchunk;
+    int64_t b = blockIdx.x;
+    if (b < kvb) {
+        gated_dgate_block<T, D>(p.q, p.k, p.v, p.dO, p.lg, p.S, p.R, p.dlg, p.N, p.nchunk, p.group,
+                                p.scale, b);
+    } else if ((b -= kvb) < kvb) {
+        gated_rows_block<T, D, true, true>(p.v, p.dO, p.q, p.lg, p.R, p.dk, p.N, p.nchunk, p.group,
+                                           p.scale, 1.f, b);
+    } else if ((b -= kvb) < kvb) {
+        gated_rows_block<T, D, true, false>(p.k, p.q, p.dO, p.lg, p.R, p.dv, p.N, p.nchunk, p.group,
+                                            p.scale, 1.f, b);
+    } else {
+        gated_rows_block<T, D, false, true>(p.dO, p.v, p.k, p.lg, p.S, p.dq, p.N, p.nchunk, p.group,
+                                            p.scale, p.scale, b - kvb);
     }
 }
 
