@@ -403,14 +403,17 @@ gated_bwd_kernel(const __grid_constant__ GatedBwdParams prm) {
         // this thread's columns of an accumulator times rr, in place; returns their
         // dot with the same columns of row irow of `tile` (null: none)
         auto scale_part = [&](int t_acc, float rr, const uint8_t* tile) {
-            float dot = 0.f;
+            float2 dot = make_float2(0.f, 0.f);
 #pragma unroll
             for (int s = 0; s < GC / 16; ++s) {
                 float sv[16];
                 const uint32_t at = tmem + lane_base + t_acc + d0 + 16 * s;
                 tmem_load<16>(at, sv);
 #pragma unroll
-                for (int t = 0; t < 16; ++t) sv[t] *= rr;
+                for (int t = 0; t < 16; t += 2) {
+                    const float2 x = mul2(make_float2(sv[t], sv[t + 1]), make_float2(rr, rr));
+                    sv[t] = x.x, sv[t + 1] = x.y;
+                }
                 tmem_st16(at, sv);
                 if (tile) {
 #pragma unroll
@@ -420,14 +423,13 @@ gated_bwd_kernel(const __grid_constant__ GatedBwdParams prm) {
                         const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
-                            const float2 f = unpack_bf16(w[j]);
-                            dot = fmaf(f.x, sv[t + 2 * j], dot);
-                            dot = fmaf(f.y, sv[t + 2 * j + 1], dot);
+                            dot = fma2(unpack_bf16(w[j]),
+                                       make_float2(sv[t + 2 * j], sv[t + 2 * j + 1]), dot);
                         }
                     }
                 }
             }
-            return dot;
+            return dot.x + dot.y;
         };
         auto put = [&](int t_acc, uint8_t* tile) {
 #pragma unroll
@@ -489,13 +491,18 @@ gated_bwd_kernel(const __grid_constant__ GatedBwdParams prm) {
                             for (int t = 0; t < 16; t += 4) {
                                 const float4 f =
                                     *reinterpret_cast<const float4*>(tab.fac + c0 + 16 * s + t);
-                                const float r = prm.scale * rJ;
-                                const float fj[4] = {r * f.x, r * f.y, r * f.z, r * f.w};
+                                const float2 r2 = make_float2(prm.scale * rJ, prm.scale * rJ);
+                                const float2 fj[2] = {mul2(r2, make_float2(f.x, f.y)),
+                                                      mul2(r2, make_float2(f.z, f.w))};
 #pragma unroll
-                                for (int w = 0; w < 4; ++w) {
-                                    pv[t + w] *= fj[w];
-                                    ms[t + w] = pv[t + w] * wv[t + w];
-                                    wv[t + w] *= fj[w];
+                                for (int w = 0; w < 2; ++w) {
+                                    const int j = t + 2 * w;
+                                    const float2 p = mul2(make_float2(pv[j], pv[j + 1]), fj[w]);
+                                    const float2 x = make_float2(wv[j], wv[j + 1]);
+                                    const float2 mv = mul2(p, x), y = mul2(x, fj[w]);
+                                    pv[j] = p.x, pv[j + 1] = p.y;
+                                    ms[j] = mv.x, ms[j + 1] = mv.y;
+                                    wv[j] = y.x, wv[j + 1] = y.y;
                                 }
                             }
                         }
