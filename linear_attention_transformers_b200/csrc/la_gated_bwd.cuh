@@ -168,6 +168,11 @@ gated_bwd_kernel(const __grid_constant__ GatedBwdParams prm) {
                 for (int a = 0; a < D / 64; ++a)
                     tma_load_3d(smem + off + a * rows * 128, map, bar, 64 * a, row, head);
             };
+            // D = 128: the tiles of the next item, brought to L2 while this one's space
+            // is still taken
+            auto ahead = [&](const CUtensorMap* map, int row, int head) {
+                for (int a = 0; a < D / 64; ++a) tma_prefetch_3d(map, 64 * a, row, head);
+            };
             uint32_t m = 0, u = 0;              // items, (item, query head) steps
             uint32_t kvn = 0, qdn = 0, srn = 0;  // issued
             bool ok = true;
@@ -197,6 +202,23 @@ gated_bwd_kernel(const __grid_constant__ GatedBwdParams prm) {
                             load(Cfg::OFF_SR + Cfg::ST, &prm.tm_r, sr_full, D, 0,
                                  head * prm.nblk + blk);
                         ++srn;
+                    }
+                    if (D == 128) {
+                        const bool same = g + 1 < G;
+                        const int64_t nx = same ? it : it + gridDim.x;
+                        if (nx < prm.items) {
+                            const int h2 = head_of(nx), b2 = blk_of(nx), qh = h2 * G + (same ? g + 1 : 0);
+                            ahead(&prm.tm_q, b2 * C, qh);
+                            ahead(&prm.tm_do, b2 * C, qh);
+                            if (!same) {
+                                ahead(&prm.tm_k, b2 * C, h2);
+                                ahead(&prm.tm_v, b2 * C, h2);
+                                if (STATE) {
+                                    ahead(&prm.tm_s, 0, h2 * prm.nblk + b2);
+                                    ahead(&prm.tm_r, 0, h2 * prm.nblk + b2);
+                                }
+                            }
+                        }
                     }
                 }
             }

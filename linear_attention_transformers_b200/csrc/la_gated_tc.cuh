@@ -103,6 +103,12 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
     return __all_sync(0xffffffffu, sm100::mbar_wait(bar, parity, abort));
 }
 
+// A box of a tensor map to L2 only.
+__device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap* map, int c0, int c1, int c2) {
+    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global [%0, {%1, %2, %3}];" ::"l"(map), "r"(c0),
+                 "r"(c1), "r"(c2)
+                 : "memory");
+}
 // Two float32 operations an instruction (each rounded as the single one is).
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
     float2 r;
