@@ -435,8 +435,8 @@ LA_EXPORT la_status la_backward_sp_dkdv(const void *q, const void *k, const void
  *
  * q, o, dO, dq: [B, H, N, D]; k, v, dk, dv: [B, Hkv, N, D]; log_gate and
  * dlog_gate: [B, Hkv, N], which need no more alignment than their elements;
- * all of dtype `dt`.  Hkv divides H, and query head h
- * reads key/value head h / (H / Hkv), as in la_forward_gqa.  S_in (may be
+ * all of dtype `dt`.  Hkv divides H, and query head h reads key/value head
+ * h / (H / Hkv), as in la_forward_gqa.  S_in (may be
  * NULL: zero) is the state before the first token and S_out (may be NULL)
  * receives the state after the last, float32 [B, Hkv, D, D] (row = key
  * feature), so a sequence can be taken in pieces and handed to
@@ -445,15 +445,19 @@ LA_EXPORT la_status la_backward_sp_dkdv(const void *q, const void *k, const void
  * log_gate is the natural logarithm of a gate in [0, 1]: at most 0, and -inf
  * drops the state (a packed document's first token).  Values above 0 are not
  * looked for; the state then grows as the recurrence says, until float32
- * overflows.  Sums of log gates are held in 64 bits.  A gate below 2^-160 is
- * taken as 0.  dlog_gate is the gradient with respect to log_gate (0 where
- * the gate is 0).
+ * overflows.  Sums of log gates are held in 64 bits, or in 32 counted from the
+ * end that a weight is measured from.  A gate below 2^-126 may be taken as 0.
+ * dlog_gate is the gradient with respect to log_gate (0 where the gate is 0).
  *
  * la_backward_gated: gradients of sum(dO * O) + sum(dS_out * S_out) with
  * respect to q, k, v, log_gate and S_in (dS_in, may be NULL).  dS_out may be
- * NULL (zero).  The gradients must not overlap the inputs or each other.  The
- * gradients of shared heads are added within the kernels, in a fixed order;
- * every call is bitwise repeatable.
+ * NULL (zero).  The outputs of both calls must not overlap the inputs or each
+ * other.  The gradients of shared heads are added within the kernels, in a
+ * fixed order; every call is bitwise repeatable.
+ *
+ * Inputs are finite: a value that is not (a product of two that overflows
+ * float32 among them) may reach every output of its 128 tokens, those before it
+ * included, and every later one.
  *
  * Types and sizes as la_forward's.  bf16 inputs are read exactly; the state
  * and all sums are float32.  Workspace: la_workspace_size_gated (0 for

@@ -48,20 +48,22 @@ GatedPlan plan_gated(la_op op, int64_t B, int64_t Hkv, int64_t N, int64_t D) {
 struct GatedTcPlan {
     int64_t nblk = 0;
     int nb = 0, nspan = 0;
-    int chain = 0;  // value columns a CTA of the walk takes; 0: spans in parallel
+    // value columns a CTA of the walk takes, for S and for R; 0: spans in parallel
+    int chain = 0, chain_r = 0;
     size_t rec = 0, tot = 0, s_enter = 0, r_enter = 0, bytes = 0;
 };
 
 // How the border states are formed: spans in parallel (0; two launches and the
 // float32 records) or a walk of CTAs of 64 or 32 value columns, whichever the
-// model below says is sooner, in us.  Measured (spans; walk with 64; with 32):
-// 128 heads of 8192 tokens, D = 64: 117, 97, 117; 64 of 4096, D = 128: 61, 54,
-// 65; 32 of 131072, D = 128: 811, 1435, 904; 8 of 777, D = 128: 20, 21, 15.
-int pick_chain(int64_t kvh, int64_t nblk, int64_t D) {
-    const double sms = num_sms();
-    const double spans = 10.0 + double(kvh) * double(nblk) * (D == 64 ? 0.0134 : 0.0243);
-    const double w64 = 4.0 + ceil(double(kvh) * double(D / 64) / sms) * double(nblk) * 1.5;
-    const double w32 = 4.0 + ceil(double(kvh) * double(D / 32) / sms) * double(nblk) * 0.9;
+// model below says is sooner, in us.  G: tiles a block (a group's query heads,
+// for R).  Measured (spans; walk with 64; with 32): 128 heads of 8192 tokens, D =
+// 64: 117, 97, 117; 64 of 4096, D = 128: 61, 54, 65; 32 of 131072, D = 128: 811,
+// 1435, 904; 8 of 777, D = 128: 20, 21, 15.
+int pick_chain(int64_t kvh, int64_t nblk, int64_t D, int64_t G) {
+    const double sms = num_sms(), tiles = double(nblk) * double(G);
+    const double spans = 10.0 + double(kvh) * tiles * (D == 64 ? 0.0134 : 0.0243);
+    const double w64 = 4.0 + ceil(double(kvh) * double(D / 64) / sms) * tiles * 1.5;
+    const double w32 = 4.0 + ceil(double(kvh) * double(D / 32) / sms) * tiles * 0.9;
     if (spans <= w64 && spans <= w32) return 0;
     return w64 <= w32 ? 64 : 32;
 }
@@ -71,17 +73,17 @@ GatedTcPlan plan_gated_tc(la_op op, int64_t B, int64_t H, int64_t Hkv, int64_t N
     p.nblk = (N + la::kGtC - 1) / la::kGtC;
     // A sequence of one span needs no border states, so up to four blocks are
     // one.  Longer spans move fewer state bytes (D^2 a span) and take more C x C
-    // products (nb + 1 over 2 a block): D = 128 gains from two blocks (131072
-    // tokens, 32 heads, forward: 2161 us with one, 1952 with two, 2083 with
-    // four), D = 64, whose states are a quarter, does not (8192 tokens, 128
-    // heads, backward: 883, 1026, 1169 us).
+    // products (nb + 1 over 2 a block) and more of L2: states and outputs of
+    // 131072 tokens, 32 heads, D = 128 take 2024 us with one block a span, 1723
+    // with two, 1866 with four; of 8192 tokens, 128 heads, D = 64: 209, 240, 273.
     // The backward kernels take single blocks.
     if (op == LA_OP_BACKWARD)
         p.nb = 1;
     else
         p.nb = p.nblk <= 1 ? 1 : p.nblk == 2 ? 2 : p.nblk <= 4 ? 4 : D == 64 ? 1 : 2;
     p.nspan = int((p.nblk + p.nb - 1) / p.nb);
-    p.chain = pick_chain(B * Hkv, p.nblk, D);
+    p.chain = pick_chain(B * Hkv, p.nblk, D, 1);
+    p.chain_r = op == LA_OP_BACKWARD ? pick_chain(B * Hkv, p.nblk, D, H / Hkv) : p.chain;
     size_t at = 0;
     auto take = [&](size_t n) {
         const size_t o = at;
@@ -89,14 +91,12 @@ GatedTcPlan plan_gated_tc(la_op op, int64_t B, int64_t H, int64_t Hkv, int64_t N
         return o;
     };
     const size_t states = size_t(B) * size_t(Hkv) * size_t(p.nspan) * size_t(D * D);
-    if (!p.chain) {
+    if (!p.chain || !p.chain_r) {
         p.rec = take(states * 4);
         p.tot = take(size_t(B) * size_t(Hkv) * size_t(p.nspan) * 4);
     }
     p.s_enter = take(states * 2);
-    if (op == LA_OP_BACKWARD) {
-        p.r_enter = take(states * 2);
-    }
+    if (op == LA_OP_BACKWARD) p.r_enter = take(states * 2);
     p.bytes = at;
     return p;
 }
@@ -198,10 +198,11 @@ la_status gated_tc_states(const void* A, const void* Bm, const void* lg, const G
                           char* ws, size_t enter, const float* first, float* last, int64_t heads,
                           int64_t kvh, int64_t N, int group, float mul, cudaStream_t st) {
     la_status s;
-    if (p.chain == 32)
+    const int chain = REV ? p.chain_r : p.chain;
+    if (chain == 32)
         return gated_tc_chain<D, 32, REV>(A, Bm, lg, p, ws, enter, first, last, heads, kvh, N,
                                           group, mul, st);
-    if (p.chain)
+    if (chain)
         return gated_tc_chain<D, 64, REV>(A, Bm, lg, p, ws, enter, first, last, heads, kvh, N,
                                           group, mul, st);
     const int run = last ? p.nspan : p.nspan - 1;

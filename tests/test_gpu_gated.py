@@ -30,6 +30,7 @@ SHAPES = [
     (1, 4, 1, 511, True, True),
     (1, 5, 5, 777, False, True),
     (1, 2, 2, 1000, True, False),
+    (1, 4, 1, 1500, True, True),
 ]
 
 
@@ -77,6 +78,32 @@ def test_forward(dtype, D, shape):
 def test_backward(dtype, D, shape):
     B, H, Hkv, N, state, resets = shape
     check_bwd(dtype, tensors(B, H, Hkv, N, D, dtype, 2 * N + D, resets), D ** -0.5, state)
+
+
+@pytest.mark.parametrize("shape", [(32, 4, 4, 400), (20, 12, 6, 300), (1, 8, 8, 3000), (2, 32, 1, 2049),
+                                   (150, 1, 1, 129)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_many_heads_and_long_ones(D, shape):
+    # the ways the states are formed that the oracle's sizes do not reach, against the
+    # float32 kernels (held to the oracle above) on the same values
+    B, H, Hkv, N = shape
+    bf, f32 = torch.bfloat16, torch.float32
+    ins = tensors(B, H, Hkv, N, D, bf, N, resets=True)
+    q, k, v, lg, dO, S, dS = ins
+    wide = [x.float() for x in (q, k, v, lg, dO)]
+    o, S_out = api.la_forward_gated(q, k, v, lg, 0.1, S, return_state=True)
+    ro, rS = api.la_forward_gated(*wide[:4], 0.1, S, return_state=True)
+    close(o, ro.cpu(), REL[bf], MAX[bf], "o")
+    close(S_out, rS.cpu(), REL_STATE[bf], 4 * REL_STATE[bf], "S")
+    got = api.la_backward_gated(q, k, v, lg, dO, 0.1, S, dS, return_dstate=True)
+    ref = api.la_backward_gated(*wide, 0.1, S, dS, return_dstate=True)
+    for n, g, r in zip(("dq", "dk", "dv", "dlog_gate"), got, ref):
+        close(g, r.cpu(), REL[bf], MAX[bf], n)
+    close(got[4], ref[4].cpu(), REL_STATE[bf], 4 * REL_STATE[bf], "dS_in")
+    torch.cuda.synchronize()
+    api.la_get_device_error()
+    plain = api.la_forward_gated(q, k, v, lg, 0.1)
+    close(plain, api.la_forward_gated(*wide[:4], 0.1).cpu(), REL[bf], MAX[bf], "o without a state")
 
 
 @pytest.mark.parametrize("gate", [0.0, -1e-3, -5.0, -80.0, -300.0, -math.inf])
