@@ -51,6 +51,9 @@ struct GatedTcPlan {
     // value columns a CTA of the walk takes, for S and for R; 0: spans in parallel
     int chain = 0, chain_r = 0;
     size_t rec = 0, tot = 0, s_enter = 0, r_enter = 0, bytes = 0;
+    // parts of <S, R> a block of the backward adds up, and where they are
+    int ndots = 0;
+    size_t dots = 0, dots_bytes = 0;
 };
 
 // How the border states are formed: spans in parallel (0; two launches and the
@@ -96,7 +99,12 @@ GatedTcPlan plan_gated_tc(la_op op, int64_t B, int64_t H, int64_t Hkv, int64_t N
         p.tot = take(size_t(B) * size_t(Hkv) * size_t(p.nspan) * 4);
     }
     p.s_enter = take(states * 2);
-    if (op == LA_OP_BACKWARD) p.r_enter = take(states * 2);
+    if (op == LA_OP_BACKWARD) {
+        p.r_enter = take(states * 2);
+        p.ndots = int(p.chain_r ? 8 * D / p.chain_r : D * D / 128);
+        p.dots_bytes = size_t(B) * size_t(Hkv) * size_t(p.nspan) * size_t(p.ndots) * 4;
+        p.dots = take(p.dots_bytes);
+    }
     p.bytes = at;
     return p;
 }
@@ -170,23 +178,27 @@ la_status gated_states(la::GatedPartJob f, la::GatedCarryJob fc, la::GatedPartJo
 }
 
 // ---------------------------------------------------- the tensor-core kernels
-template <int D, int EC, bool REV>
+template <int D, int EC, bool REV, int SPLIT>
 la_status gated_tc_chain(const void* A, const void* Bm, const void* lg, const GatedTcPlan& p,
                          char* ws, size_t enter, const float* first, float* last, int64_t heads,
                          int64_t kvh, int64_t N, int group, float mul, cudaStream_t st) {
-    using Cfg = la::GatedChainCfg<D, EC>;
+    using Cfg = la::GatedChainCfg<D, EC, SPLIT>;
     la_status s;
     la::GatedChainParams prm;
     memset(&prm, 0, sizeof(prm));
     if (!make_qkv_map(&prm.tm_a, A, heads, N, D, la::kGtC)) return LA_ERR_CUDA;
     prm.b = static_cast<const __nv_bfloat16*>(Bm), prm.lg = static_cast<const __nv_bfloat16*>(lg);
     prm.first = first, prm.last = last;
+    if (REV && p.dots_bytes) {
+        prm.S = reinterpret_cast<const __nv_bfloat16*>(ws + p.s_enter);
+        prm.dots = reinterpret_cast<float*>(ws + p.dots);
+    }
     prm.enter = reinterpret_cast<__nv_bfloat16*>(ws + enter);
     prm.N = N, prm.nblk = int(p.nblk), prm.nb = p.nb, prm.nspan = p.nspan, prm.group = group;
     prm.mul = mul;
     // without `last` the span walked last adds nothing that is asked for
     prm.blocks = last ? prm.nblk : REV ? std::max(0, prm.nblk - p.nb) : (p.nspan - 1) * p.nb;
-    auto kern = la::gated_chain_kernel<D, EC, REV>;
+    auto kern = la::gated_chain_kernel<D, EC, REV, SPLIT>;
     if ((s = allow_smem(kern, Cfg::SMEM)) != LA_OK) return s;
     la::LaunchScope scope(REV ? "gated_chain_rev" : "gated_chain", st);
     kern<<<unsigned(kvh * (D / EC)), la::kGatedChainThreads, Cfg::SMEM, st>>>(prm);
@@ -199,17 +211,21 @@ la_status gated_tc_states(const void* A, const void* Bm, const void* lg, const G
                           int64_t kvh, int64_t N, int group, float mul, cudaStream_t st) {
     la_status s;
     const int chain = REV ? p.chain_r : p.chain;
+    auto walk = [&](auto ec, auto split) {
+        return gated_tc_chain<D, decltype(ec)::value, REV, decltype(split)::value>(
+            A, Bm, lg, p, ws, enter, first, last, heads, kvh, N, group, mul, st);
+    };
+    using std::integral_constant;
     if (chain == 32)
-        return gated_tc_chain<D, 32, REV>(A, Bm, lg, p, ws, enter, first, last, heads, kvh, N,
-                                          group, mul, st);
+        return last ? walk(integral_constant<int, 32>{}, integral_constant<int, 3>{})
+                    : walk(integral_constant<int, 32>{}, integral_constant<int, 2>{});
     if (chain)
-        return gated_tc_chain<D, 64, REV>(A, Bm, lg, p, ws, enter, first, last, heads, kvh, N,
-                                          group, mul, st);
+        return last ? walk(integral_constant<int, 64>{}, integral_constant<int, 3>{})
+                    : walk(integral_constant<int, 64>{}, integral_constant<int, 2>{});
     const int run = last ? p.nspan : p.nspan - 1;
     float* rec = reinterpret_cast<float*>(ws + p.rec);
     float* tot = reinterpret_cast<float*>(ws + p.tot);
     if (run > 0) {
-        using Cfg = la::GatedSpanCfg<D>;
         la::GatedSpanParams prm;
         memset(&prm, 0, sizeof(prm));
         if (!make_qkv_map(&prm.tm_a, A, heads, N, D, la::kGtC) ||
@@ -220,20 +236,27 @@ la_status gated_tc_states(const void* A, const void* Bm, const void* lg, const G
         prm.items = kvh * run, prm.nspan = p.nspan, prm.spans_run = run;
         prm.span0 = REV && !last ? 1 : 0;
         prm.nb = p.nb, prm.nblk = int(p.nblk), prm.group = group, prm.mul = mul;
-        auto kern = la::gated_span_kernel<D, REV>;
-        if ((s = allow_smem(kern, Cfg::SMEM)) != LA_OK) return s;
-        const unsigned grid = unsigned(std::min<int64_t>(prm.items, int64_t(num_sms()) * Cfg::CTAS));
-        la::LaunchScope scope(REV ? "gated_span_rev" : "gated_span", st);
-        kern<<<grid, la::kGatedSpanThreads, Cfg::SMEM, st>>>(prm);
-        if ((s = launch_status()) != LA_OK) return s;
+        auto go = [&](auto split) -> la_status {
+            using Cfg = la::GatedSpanCfg<D, decltype(split)::value>;
+            auto kern = la::gated_span_kernel<D, REV, decltype(split)::value>;
+            if (la_status e = allow_smem(kern, Cfg::SMEM)) return e;
+            const unsigned grid =
+                unsigned(std::min<int64_t>(prm.items, int64_t(num_sms()) * Cfg::CTAS));
+            la::LaunchScope scope(REV ? "gated_span_rev" : "gated_span", st);
+            kern<<<grid, la::kGatedSpanThreads, Cfg::SMEM, st>>>(prm);
+            return launch_status();
+        };
+        s = last ? go(std::integral_constant<int, 3>{}) : go(std::integral_constant<int, 2>{});
+        if (s != LA_OK) return s;
     }
     const int per = D * D / 4;
     const int64_t total = kvh * per;
     la::LaunchScope scope(REV ? "gated_border_rev" : "gated_border", st);
     la::gated_border_kernel<REV><<<unsigned((total + 127) / 128), 128, 0, st>>>(
         reinterpret_cast<const float4*>(rec), tot, reinterpret_cast<const float4*>(first),
-        reinterpret_cast<float4*>(last), reinterpret_cast<uint2*>(ws + enter), total, per,
-        p.nspan);
+        reinterpret_cast<float4*>(last), reinterpret_cast<uint2*>(ws + enter),
+        REV && p.dots_bytes ? reinterpret_cast<const uint2*>(ws + p.s_enter) : nullptr,
+        reinterpret_cast<float*>(ws + p.dots), total, per, p.nspan);
     return launch_status();
 }
 
@@ -277,12 +300,13 @@ la_status run_gated_bwd_tc(const void* q, const void* k, const void* v, const vo
                            void* dk, void* dv, void* dlg, float* dS_in, float scale, int64_t B,
                            int64_t H, int64_t Hkv, int64_t N, char* ws, cudaStream_t st) {
     la_status s;
-    const GatedTcPlan p = plan_gated_tc(LA_OP_BACKWARD, B, H, Hkv, N, D);
+    GatedTcPlan p = plan_gated_tc(LA_OP_BACKWARD, B, H, Hkv, N, D);
     const int group = int(H / Hkv);
     const int64_t kvh = B * Hkv, qh = B * H;
     // the blocks take both border states or, a single block that nothing enters
     // or leaves, none
     const bool state = p.nspan > 1 || S_in || dS_out;
+    if (!state) p.dots_bytes = 0;  // S is not formed
     if (state && (s = gated_tc_states<D, false>(k, v, lg, p, ws, p.s_enter, S_in, nullptr, kvh, kvh,
                                                 N, 1, 1.f, st)) != LA_OK)
         return s;
@@ -302,6 +326,7 @@ la_status run_gated_bwd_tc(const void* q, const void* k, const void* v, const vo
         return LA_ERR_CUDA;
     prm.lg = static_cast<const __nv_bfloat16*>(lg), prm.dlg = static_cast<__nv_bfloat16*>(dlg);
     prm.N = N, prm.items = kvh * p.nblk, prm.nblk = int(p.nblk), prm.group = group;
+    prm.dots = reinterpret_cast<const float*>(ws + p.dots), prm.ndots = p.ndots;
     prm.scale = scale;
     auto kern = state ? la::gated_bwd_kernel<D, true> : la::gated_bwd_kernel<D, false>;
     constexpr size_t kSmem = la::GatedBwdCfg<D>::SMEM;

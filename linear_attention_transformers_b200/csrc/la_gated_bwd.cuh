@@ -40,7 +40,8 @@ struct GatedBwdParams {
     const __nv_bfloat16* lg;
     __nv_bfloat16* dlg;
     int64_t N, items;   // items: key/value heads * nblk
-    int nblk, group;
+    const float* dots;  // [kvh][nblk][ndots]: parts of <S, R>
+    int nblk, group, ndots;
     float scale;
 };
 
@@ -62,7 +63,7 @@ struct GatedBwdCfg {
     static constexpr int OFF_SR = D == 64 ? OFF_PW + 2 * PT : OFF_PW;
     static constexpr int OFF_TAB = D == 64 ? OFF_SR + 2 * ST : OFF_PW + 2 * PT;
     static constexpr int OFF_RED = OFF_TAB + 2 * int(sizeof(GateTabBlock));
-    static constexpr int RED = 12 * C + 16;              // rows [4], cols [4], through [4], <S, R> [16]
+    static constexpr int RED = 12 * C;                   // rows [4], cols [4], through [4]
     static constexpr int OFF_BAR = OFF_RED + RED * 4;
     static constexpr int NBAR = 26;
     static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
@@ -98,7 +99,7 @@ gated_bwd_kernel(const __grid_constant__ GatedBwdParams prm) {
     uint64_t* sr_full = bars + 8;    // TMA
     uint64_t* sr_free = bars + 9;    // S, R (D = 128: and P~, W~) read    (commit)
     uint64_t* pw_raw = bars + 10;    // P, W complete                      (commit)
-    uint64_t* p_read = bars + 11;    // P, W in registers; <S, R> formed   (16 warps)
+    uint64_t* p_read = bars + 11;    // P, W in registers                  (16 warps)
     uint64_t* s_full = bars + 12;    // products with S and R complete     (commit)
     uint64_t* pw_full = bars + 13;   // P~, W~ packed, state parts scaled  (16 warps)
     uint64_t* a_full = bars + 14;    // dq, dk complete                    (commit)
@@ -337,9 +338,13 @@ gated_bwd_kernel(const __grid_constant__ GatedBwdParams prm) {
                     break;
                 tables(it + gridDim.x, nb);
             }
-            const float eall = ex2_fast(float(tabs[m & 1].start[4]));
+            float x = 0.f;  // e^{G_C} <S, R>
+            if (STATE) {
+                const float* dots = prm.dots + it * prm.ndots;
+                for (int i = lane; i < prm.ndots; i += 32) x += dots[i];
+                x = warp_sum(x) * ex2_fast(float(tabs[m & 1].start[4]));
+            }
             if (!(ok = warp_wait(kv_out, m & 1, abort_flag))) break;
-            const float x = STATE ? eall * warp_sum(lane < 16 ? red[12 * C + lane] : 0.f) : 0.f;
             // tokens 4 l .. 4 l + 3 of lane l
             float d[4], t[4], ds = 0.f, ts = 0.f;
 #pragma unroll
@@ -470,25 +475,9 @@ gated_bwd_kernel(const __grid_constant__ GatedBwdParams prm) {
             const float r_k = ex2_fast(float(tab.start[4] - gI) - gi);
             const int J = grp;
             const float rJ = J < sp ? ex2_fast(gi + float(gI - tab.start[J + 1])) : 0.f;
-            float rsum = 0.f, csum = 0.f, through = 0.f, sr = 0.f;
+            float rsum = 0.f, csum = 0.f, through = 0.f;
             uint8_t* kt = smem + Cfg::OFF_KV + (m % NB) * 2 * TILE;
             for (int g = 0; g < G; ++g, ++u) {
-                if (STATE && g == 0) {  // <S, R>: same swizzle, same places
-                    if (!(ok = wait(sr_full, u & 1))) break;
-                    const uint4* s4 = reinterpret_cast<const uint4*>(smem + Cfg::OFF_SR) + (tid - 128);
-                    const uint4* r4 = s4 + Cfg::ST / 16;
-#pragma unroll
-                    for (int i = 0; i < D * D / 8 / kGatedBwdWork; ++i) {
-                        const uint4 a = s4[i * kGatedBwdWork], b = r4[i * kGatedBwdWork];
-                        const uint32_t p[4] = {a.x, a.y, a.z, a.w}, q[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const float2 f = unpack_bf16(p[j]), h = unpack_bf16(q[j]);
-                            sr = fmaf(f.x, h.x, sr);
-                            sr = fmaf(f.y, h.y, sr);
-                        }
-                    }
-                }
                 if (!(ok = wait(pw_raw, u & 1))) break;
                 tc_fence_after();
                 uint32_t mp[16], pp[16], wp[16];  // M, P~, W~ in bf16 pairs
@@ -617,8 +606,6 @@ gated_bwd_kernel(const __grid_constant__ GatedBwdParams prm) {
             red[grp * C + irow] = rsum;
             red[(4 + sp) * C + c0 + lane] = csum;
             red[(8 + grp) * C + irow] = through;
-            sr = warp_sum(sr);
-            if (lane == 0) red[12 * C + warp - 4] = sr;
             fence_proxy_async_smem();
             tc_fence_before();
             warp_arrive(kv_read);

@@ -12,8 +12,14 @@
 //     S <- e^{G_C} S + A^T (w B),     w_t = e^{G_C - G_t}  (REV: mul e^{G_t})
 //
 // with A the block's keys (REV: queries), read through a TMA ring, and B the
-// values (dO), read by the threads that scale them and write them as two bf16
-// parts side by side: one MMA of M = D, N = 2 EC per 16 tokens.
+// values (dO), read by the threads that scale them and write them as bf16 parts
+// side by side: one MMA of M = D, N = SPLIT EC per 16 tokens.  Two parts (2^-17
+// of the value) where the state only enters the blocks, as bf16; three (2^-24)
+// where the caller is given it in float32.
+//
+// REV with S (the states entering the blocks, formed before): also the sums
+// <S, R> that dlog_gate needs, from R in float32, since R in bf16 as well would
+// put two roundings into a sum that dlog_gate often mostly is.
 //
 // The steps of a block (scale, products, update) belong to different warps and
 // overlap across blocks; a block takes as long as the longest of them, the scale
@@ -32,17 +38,21 @@ struct GatedChainParams {
     const float* first;        // [kvh][D][D] or null
     float* last;               // [kvh][D][D] or null
     __nv_bfloat16* enter;      // [kvh][nspan][D][D]
+    const __nv_bfloat16* S;    // REV: the forward's `enter`, or null
+    float* dots;               // REV: [kvh][nspan][D / EC * 8] parts of <S, R>
     int64_t N;
     int nblk, nb, nspan, group, blocks;  // blocks: walked (the last span may be left out)
     float mul;
 };
 
-template <int D, int EC>
+template <int D, int EC, int SPLIT>
 struct GatedChainCfg {
     static constexpr int TILE = kGtC * D * 2;          // A
-    static constexpr int NS = D == 128 && EC == 64 ? 3 : 4;
-    static constexpr int SC = kGtC * 2 * EC * 2;       // scaled B: hi | lo
-    static constexpr int NB = NS;                      // blocks of B on their way
+    // ring of A, tiles of B on their way: what fits beside the scaled parts
+    static constexpr int NS = (D == 128 && EC == 64 ? 3 : 4) -
+                              (SPLIT == 3 && (D == 128 || EC == 64) ? 1 : 0);
+    static constexpr int SC = kGtC * 128 * ((SPLIT * EC + 63) / 64);  // scaled B, 64-column atoms
+    static constexpr int NB = NS;
     static constexpr int OFF_SC = NS * TILE;           // [2]
     static constexpr int OFF_B = OFF_SC + 2 * SC;      // [NB][EC / 16][256 threads] 16 bytes
     static constexpr int OFF_W = OFF_B + NB * kGtC * EC * 2;  // [4][128] weights
@@ -51,19 +61,19 @@ struct GatedChainCfg {
     static constexpr int NBAR = 2 * NS + 17;
     static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
     static constexpr int SMEM = OFF_MISC + 16 + 1024;
-    static constexpr int ACC = 2 * EC;
-    static constexpr int T_COLS = 2 * ACC;             // 128 or 256
+    static constexpr int ACC = SPLIT * EC;
+    static constexpr int T_COLS = 2 * ACC <= 128 ? 128 : 2 * ACC <= 256 ? 256 : 512;
     static_assert(SMEM <= 227 * 1024, "shared memory budget");
 };
 
 // Warps: 0 TMA, 1 MMA, 2 gates, 3 idle, 4-11 scale, 12-19 update.
 constexpr int kGatedChainThreads = 640;
 
-template <int D, int EC, bool REV>
+template <int D, int EC, bool REV, int SPLIT>
 __global__ void __launch_bounds__(kGatedChainThreads, 1)
 gated_chain_kernel(const __grid_constant__ GatedChainParams prm) {
     using namespace sm100;
-    using Cfg = GatedChainCfg<D, EC>;
+    using Cfg = GatedChainCfg<D, EC, SPLIT>;
     constexpr int C = kGtC, NS = Cfg::NS;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -74,9 +84,9 @@ gated_chain_kernel(const __grid_constant__ GatedChainParams prm) {
     uint64_t* sc_full = empty + NS;     // [2] scaled                     (8 warps)
     uint64_t* sc_free = sc_full + 2;    // [2] products done              (commit)
     uint64_t* acc_full = sc_full + 4;   // [2] a block's sum complete     (commit)
-    uint64_t* acc_free = sc_full + 6;   // [2] ... read                   (8 warps)
+    uint64_t* acc_free = sc_full + 6;   // [2] ... read                   (update warps)
     uint64_t* w_full = sc_full + 8;     // [4] weights written            (1)
-    uint64_t* w_free = sc_full + 12;    // [4] ... read (8 scale warps, 8 update warps)
+    uint64_t* w_free = sc_full + 12;    // [4] ... read (scale and update warps)
     uint64_t* drain = sc_full + 16;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Cfg::OFF_MISC);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Cfg::OFF_MISC + 4);
@@ -139,7 +149,7 @@ gated_chain_kernel(const __grid_constant__ GatedChainParams prm) {
         }
     } else if (warp == 1) {
         const uint32_t one = elect_lane();
-        constexpr uint32_t id = idesc_bf16(D, 2 * EC, 1, 1);
+        constexpr uint32_t id = idesc_bf16(D, SPLIT * EC, 1, 1);
         uint32_t n = 0;
         bool ok = true;
         for (int i = 0; ok && i < steps; ++i) {
@@ -270,19 +280,23 @@ gated_chain_kernel(const __grid_constant__ GatedChainParams prm) {
                 uint8_t* sc = smem + Cfg::OFF_SC + (n & 1) * Cfg::SC;
 #pragma unroll
                 for (int j = 0; j < NV; ++j) {
-                    uint32_t hi[4] = {x[j].x, x[j].y, x[j].z, x[j].w}, lo[4];
+                    uint32_t part[SPLIT][4];
+                    const uint32_t raw[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
-                        const float2 f = mul2(unpack_bf16(hi[c]), make_float2(w, w));
-                        hi[c] = pack_bf16(f.x, f.y);
-                        const float2 r = fma2(unpack_bf16(hi[c]), make_float2(-1.f, -1.f), f);
-                        lo[c] = pack_bf16(r.x, r.y);
+                        float2 f = mul2(unpack_bf16(raw[c]), make_float2(w, w));
+#pragma unroll
+                        for (int i2 = 0; i2 < SPLIT; ++i2) {
+                            part[i2][c] = pack_bf16(f.x, f.y);
+                            if (i2 + 1 < SPLIT)
+                                f = fma2(unpack_bf16(part[i2][c]), make_float2(-1.f, -1.f), f);
+                        }
                     }
-                    const int q = h * NV + j;
-                    *reinterpret_cast<uint4*>(sc + tile_chunk_off(C, row, q)) =
-                        make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                    *reinterpret_cast<uint4*>(sc + tile_chunk_off(C, row, q + EC / 8)) =
-                        make_uint4(lo[0], lo[1], lo[2], lo[3]);
+#pragma unroll
+                    for (int i2 = 0; i2 < SPLIT; ++i2)
+                        *reinterpret_cast<uint4*>(
+                            sc + tile_chunk_off(C, row, h * NV + j + i2 * (EC / 8))) =
+                            make_uint4(part[i2][0], part[i2][1], part[i2][2], part[i2][3]);
                 }
                 fence_proxy_async_smem();
                 warp_arrive(&sc_full[n & 1]);
@@ -304,7 +318,36 @@ gated_chain_kernel(const __grid_constant__ GatedChainParams prm) {
                                              : make_float4(0.f, 0.f, 0.f, 0.f);
             run[j] = x.x, run[j + 1] = x.y, run[j + 2] = x.z, run[j + 3] = x.w;
         }
+        // S of the span that is written next, loaded one ahead
+        uint4 sx[REV ? W / 8 : 1];
+        auto fetch_s = [&](int span) {
+            if (!REV || !prm.S || d < 0 || span < 0) return;
+            const uint4* s4 = reinterpret_cast<const uint4*>(
+                prm.S + (int64_t(head) * prm.nspan + span) * D * D + at);
+#pragma unroll
+            for (int j = 0; j < W / 8; ++j) sx[j] = __ldcs(s4 + j);
+        };
+        fetch_s(prm.nspan - 1);
         auto put = [&](int span) {
+            if (REV && prm.S) {  // this thread's share of <S, R>, a value a warp
+                float2 d2 = make_float2(0.f, 0.f);
+                if (d >= 0) {
+#pragma unroll
+                    for (int j = 0; j < W / 8; ++j) {
+                        const uint4 x = sx[j];
+                        const uint32_t p[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+                            d2 = fma2(unpack_bf16(p[c]),
+                                      make_float2(run[8 * j + 2 * c], run[8 * j + 2 * c + 1]), d2);
+                    }
+                }
+                fetch_s(span - 1);
+                const float dot = warp_sum(d2.x + d2.y);
+                if (lane == 0)
+                    prm.dots[((int64_t(head) * prm.nspan + span) * NPART + int(blockIdx.x) % NPART) * 8 +
+                             warp - 12] = dot;
+            }
             if (d < 0) return;
             __nv_bfloat16* out = prm.enter + (int64_t(head) * prm.nspan + span) * D * D + at;
 #pragma unroll
@@ -328,6 +371,12 @@ gated_chain_kernel(const __grid_constant__ GatedChainParams prm) {
                 float hi[16], lo[16];
                 tmem_ld16(acc + j, hi);
                 tmem_load<16>(acc + EC + j, lo);
+                if (SPLIT == 3) {
+                    float l2[16];
+                    tmem_load<16>(acc + 2 * EC + j, l2);
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) lo[c] += l2[c];
+                }
 #pragma unroll
                 for (int c = 0; c < 16; ++c) run[j + c] = fmaf(a, run[j + c], hi[c] + lo[c]);
             }

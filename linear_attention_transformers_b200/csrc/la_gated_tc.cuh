@@ -27,9 +27,9 @@
 //
 // Rounding.  q, k, v, dO are read exactly.  The weighted C x C product and the
 // border states are rounded to bf16 once, as tensor-core operands; the scaled
-// operand of the parts is held as two bf16 values (hi + lo, 2^-17), so that
-// the float32 states returned to the caller keep float32 accuracy; the row
-// factors of what comes through a state are applied to the float32 result.
+// operand of the parts is held as two bf16 values, or three where a state goes
+// to the caller in float32; the row factors of what comes through a state are
+// applied to the float32 result.
 #pragma once
 
 #include "la_chunk_fwd.cuh"
@@ -182,18 +182,17 @@ struct GatedSpanParams {
     float mul;
 };
 
-template <int D>
+template <int D, int SPLIT>
 struct GatedSpanCfg {
     static constexpr int TILE = kGtC * D * 2;
     static constexpr int NS = 4;                      // ring slots: A, B, A, B
-    static constexpr int OFF_SC = NS * TILE;          // the scaled operand: hi tile, lo tile
-    static constexpr int OFF_W = OFF_SC + 2 * TILE;   // weights [2][512]
+    static constexpr int OFF_LO = NS * TILE;          // the scaled operand's later parts
+    static constexpr int OFF_W = OFF_LO + (SPLIT - 1) * TILE;  // weights [2][512]
     static constexpr int OFF_BAR = OFF_W + 2 * kGtMaxNb * kGtC * 4;
     static constexpr int NBAR = 2 * NS + 11;
     static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
     static constexpr int SMEM = OFF_MISC + 16 + 1024;
-    static constexpr int ACC = 2 * D;                 // columns: hi part, lo part
-    static constexpr int T_COLS = 2 * ACC;
+    static constexpr int T_COLS = 2 * D;              // two records
     static constexpr int CTAS = D == 64 ? 2 : 1;
     static_assert(CTAS * (SMEM + 1024) <= 228 * 1024, "shared memory budget");
     static_assert(CTAS * T_COLS <= 512, "TMEM budget");
@@ -202,21 +201,24 @@ struct GatedSpanCfg {
 // Warps: 0 TMA, 1 MMA, 2 gate sums, 3 idle, 4-11 scale, 12-15 write the record.
 constexpr int kGatedSpanThreads = 512;
 
-// The accumulator is transposed, acc[e][d] = sum_t B_t[e] (w_t A_t)[d], with
-// the scaled operand's two parts side by side in columns: one MMA of N = 2 D
-// per 16 tokens, and a thread adds the two parts of its row.
-template <int D, bool REV>
-__global__ void __launch_bounds__(kGatedSpanThreads, GatedSpanCfg<D>::CTAS)
+// The accumulator is transposed, acc[e][d] = sum_t B_t[e] (w_t A_t)[d]: a thread
+// of the epilogue has one e, so a warp writes rows of the record.  The scaled
+// operand is SPLIT bf16 parts, the first over A in its ring slot, the others
+// behind the ring, with a product each into the same accumulator: two (2^-17 of
+// the value) where the states only enter the blocks, as bf16, three (2^-24) where
+// the caller is given the last in float32.
+template <int D, bool REV, int SPLIT>
+__global__ void __launch_bounds__(kGatedSpanThreads, (GatedSpanCfg<D, SPLIT>::CTAS))
 gated_span_kernel(const __grid_constant__ GatedSpanParams prm) {
     using namespace sm100;
-    using Cfg = GatedSpanCfg<D>;
+    using Cfg = GatedSpanCfg<D, SPLIT>;
     constexpr int C = kGtC, NS = Cfg::NS;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sbase = smem_u32(smem);
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + Cfg::OFF_BAR);  // [NS] TMA
-    uint64_t* empty = full + NS;       // [NS] A: scaled (8 warps); B: MMA done (commit)
+    uint64_t* empty = full + NS;       // [NS] MMAs done                  (commit)
     uint64_t* sc_full = empty + NS;    // scaled operand written          (8 warps)
     uint64_t* sc_free = sc_full + 1;   // MMAs have read it               (commit)
     uint64_t* acc_full = sc_full + 2;  // [2] record complete             (commit)
@@ -232,7 +234,7 @@ gated_span_kernel(const __grid_constant__ GatedSpanParams prm) {
     if (tid == 0) {
         for (int s = 0; s < NS; ++s) {
             mbar_init(&full[s], 1);
-            mbar_init(&empty[s], (s & 1) ? 1 : 8);
+            mbar_init(&empty[s], 1);
         }
         mbar_init(sc_full, 8);
         mbar_init(sc_free, 1);
@@ -292,13 +294,12 @@ gated_span_kernel(const __grid_constant__ GatedSpanParams prm) {
     } else if (warp == 1) {
         {
             const uint32_t one = elect_lane();
-            constexpr uint32_t id = idesc_bf16(D, 2 * D, 1, 1);
-            const uint64_t dsc = desc_mn_base(sbase + Cfg::OFF_SC, C);
+            constexpr uint32_t id = idesc_bf16(D, D, 1, 1);
             uint32_t n = 0, blk = 0, m = 0;
             bool ok = true;
             for (int64_t it = blockIdx.x; ok && it < items; it += gridDim.x, ++m) {
                 const int cnt = ng * blocks_of(span_of(it));
-                const uint32_t acc = tmem + (m & 1) * Cfg::ACC;
+                const uint32_t acc = tmem + (m & 1) * D;
                 if (m >= 2 && !(ok = warp_wait(&acc_free[m & 1], ((m >> 1) - 1) & 1, abort_flag)))
                     break;
                 for (int b = 0; b < cnt; ++b, ++blk, n += 2) {
@@ -308,8 +309,16 @@ gated_span_kernel(const __grid_constant__ GatedSpanParams prm) {
                     tc_fence_after();
                     const uint64_t db = desc_mn_base(sbase + s * Cfg::TILE, C);
 #pragma unroll
-                    for (int k = 0; k < C; k += 16)
-                        umma_one(one, acc, db + kstep_mn(k), dsc + kstep_mn(k), id, b > 0 || k > 0);
+                    for (int i = 0; i < SPLIT; ++i) {
+                        const uint64_t da = desc_mn_base(
+                            sbase + (i == 0 ? (n % NS) * Cfg::TILE : Cfg::OFF_LO + (i - 1) * Cfg::TILE),
+                            C);
+#pragma unroll
+                        for (int k = 0; k < C; k += 16)
+                            umma_one(one, acc, db + kstep_mn(k), da + kstep_mn(k), id,
+                                     b > 0 || i > 0 || k > 0);
+                    }
+                    commit_one(one, &empty[n % NS]);
                     commit_one(one, &empty[s]);
                     commit_one(one, sc_free);
                 }
@@ -341,7 +350,7 @@ gated_span_kernel(const __grid_constant__ GatedSpanParams prm) {
         // scale A's rows: thread u takes half a row (D / 2 elements)
         const int u = tid - 128;
         const int row = u >> 1, q0 = (u & 1) * (D / 16);
-        uint8_t* sc = smem + Cfg::OFF_SC;
+        uint8_t* lo = smem + Cfg::OFF_LO;
         uint32_t n = 0, blk = 0, m = 0;
         bool ok = true;
         for (int64_t it = blockIdx.x; ok && it < items; it += gridDim.x, ++m) {
@@ -355,32 +364,34 @@ gated_span_kernel(const __grid_constant__ GatedSpanParams prm) {
                 if (!(ok = __all_sync(0xffffffffu,
                                       mbar_wait(&full[s], (n / NS) & 1, abort_flag))))
                     break;
-                const uint8_t* src = smem + s * Cfg::TILE;
+                uint8_t* src = smem + s * Cfg::TILE;
                 uint4 x[D / 16];
 #pragma unroll
                 for (int i = 0; i < D / 16; ++i)
                     x[i] = *reinterpret_cast<const uint4*>(src + tile_chunk_off(C, row, q0 + i));
-                warp_arrive(&empty[s]);
                 if (!(ok = __all_sync(0xffffffffu, blk == 0 || mbar_wait(sc_free, (blk - 1) & 1,
                                                                          abort_flag))))
                     break;
                 const float wr = w[(b % nbv) * C + row];
 #pragma unroll
                 for (int i = 0; i < D / 16; ++i) {
-                    uint32_t h[4] = {x[i].x, x[i].y, x[i].z, x[i].w}, l[4];
+                    const uint32_t raw[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+                    uint32_t part[SPLIT][4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        float2 f = unpack_bf16(h[j]);
-                        f.x *= wr;
-                        f.y *= wr;
-                        h[j] = pack_bf16(f.x, f.y);
-                        const float2 r = unpack_bf16(h[j]);
-                        l[j] = pack_bf16(f.x - r.x, f.y - r.y);
+                        float2 f = mul2(unpack_bf16(raw[j]), make_float2(wr, wr));
+#pragma unroll
+                        for (int c = 0; c < SPLIT; ++c) {
+                            part[c][j] = pack_bf16(f.x, f.y);
+                            if (c + 1 < SPLIT)
+                                f = fma2(unpack_bf16(part[c][j]), make_float2(-1.f, -1.f), f);
+                        }
                     }
                     const uint32_t off = tile_chunk_off(C, row, q0 + i);
-                    *reinterpret_cast<uint4*>(sc + off) = make_uint4(h[0], h[1], h[2], h[3]);
-                    *reinterpret_cast<uint4*>(sc + Cfg::TILE + off) =
-                        make_uint4(l[0], l[1], l[2], l[3]);
+#pragma unroll
+                    for (int c = 0; c < SPLIT; ++c)
+                        *reinterpret_cast<uint4*>((c == 0 ? src : lo + (c - 1) * Cfg::TILE) + off) =
+                            make_uint4(part[c][0], part[c][1], part[c][2], part[c][3]);
                 }
                 fence_proxy_async_smem();
                 warp_arrive(sc_full);
@@ -396,16 +407,15 @@ gated_span_kernel(const __grid_constant__ GatedSpanParams prm) {
             if (!__all_sync(0xffffffffu, mbar_wait(&acc_full[m & 1], (m >> 1) & 1, abort_flag)))
                 break;
             tc_fence_after();
-            const uint32_t acc = tmem + lane_base + (m & 1) * Cfg::ACC;
+            const uint32_t acc = tmem + lane_base + (m & 1) * D;
             float* out = prm.rec + (head_of(it) * prm.nspan + span_of(it)) * int64_t(D) * D;
 #pragma unroll 1
             for (int d0 = 0; d0 < D; d0 += 16) {
-                float hi[16], lo[16];
-                tmem_ld16(acc + d0, hi);
-                tmem_load<16>(acc + D + d0, lo);
+                float x[16];
+                tmem_load<16>(acc + d0, x);
                 if (e >= 0) {
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) out[(d0 + j) * D + e] = hi[j] + lo[j];
+                    for (int j = 0; j < 16; ++j) out[(d0 + j) * D + e] = x[j];
                 }
             }
             tc_fence_before();
@@ -421,12 +431,14 @@ gated_span_kernel(const __grid_constant__ GatedSpanParams prm) {
 // --------------------------------------------------------- the spans' recurrence
 // The state entering every span in bf16 (operands of the blocks), from the
 // spans' float32 parts; run itself stays float32.  One float4 a thread.
-// `last` may be null; then the part of the span walked last is not read.
+// `last` may be null; then the part of the span walked last is not read.  Whole
+// warps: per_head is a multiple of 128.
 template <bool REV>
 __global__ void __launch_bounds__(128)
 gated_border_kernel(const float4* __restrict__ rec, const float* __restrict__ tot,
                     const float4* __restrict__ first, float4* __restrict__ last,
-                    uint2* __restrict__ enter, int64_t total, int per_head, int nspan) {
+                    uint2* __restrict__ enter, const uint2* __restrict__ S,
+                    float* __restrict__ dots, int64_t total, int per_head, int nspan) {
     const int64_t i = int64_t(blockIdx.x) * blockDim.x + threadIdx.x;
     if (i >= total) return;
     const int64_t head = i / per_head, e = i % per_head;
@@ -436,7 +448,17 @@ gated_border_kernel(const float4* __restrict__ rec, const float* __restrict__ to
     float4 run = first ? first[i] : make_float4(0.f, 0.f, 0.f, 0.f);
     constexpr int U = 8;
     const int steps = last ? nspan : nspan - 1;
+    // REV with S: a warp's share of <S, R> at the span (per_head / 32 of them), from
+    // R in float32 (see gated_chain_kernel); a warp is always within one head
     auto put = [&](int c) {
+        if (REV && S) {
+            const uint2 u = S[(head * nspan + c) * per_head + e];
+            const float2 f = sm100::unpack_bf16(u.x), h = sm100::unpack_bf16(u.y);
+            const float dot =
+                warp_sum(fmaf(f.x, run.x, fmaf(f.y, run.y, fmaf(h.x, run.z, h.y * run.w))));
+            if ((threadIdx.x & 31) == 0)
+                dots[(head * nspan + c) * (per_head / 32) + e / 32] = dot;
+        }
         out[int64_t(c) * per_head] =
             make_uint2(sm100::pack_bf16(run.x, run.y), sm100::pack_bf16(run.z, run.w));
     };

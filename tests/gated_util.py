@@ -17,8 +17,8 @@ u = 2^-8 of the value, u / sqrt(3) in the root mean square; independent, they
 give at most u in the 2-norm: REL = 2^-8.  The largest of 10^6 errors is about
 six of the typical ones beside the output's own half step: 7 u < MAX = 2^-5 of
 the largest value.  float32 outputs of bf16 inputs (states, channel sums) come
-from products of exact bf16 values and of a scaled operand held as two bf16
-parts (2^-17 of the value at most): REL = 2^-17.
+from products of exact bf16 values and of a scaled operand held as three bf16
+parts (2^-24 of the value), added in float32 as above: REL = 2^-18.
 """
 import math
 
@@ -27,7 +27,7 @@ import torch
 
 REL = {torch.float32: 2.0 ** -18, torch.bfloat16: 2.0 ** -8}
 MAX = {torch.float32: 2.0 ** -16, torch.bfloat16: 2.0 ** -5}
-REL_STATE = {torch.float32: 2.0 ** -18, torch.bfloat16: 2.0 ** -17}
+REL_STATE = {torch.float32: 2.0 ** -18, torch.bfloat16: 2.0 ** -18}
 
 
 def close(got, ref, rel, most, what):

@@ -43,8 +43,9 @@ def check_fwd(dtype, ins, scale, state, what=""):
     ro, rS = gated.forward(q, k, v, lg, scale, S)
     close(o, ro, REL[dtype], MAX[dtype], f"{what} o")
     close(S_out, rS, REL_STATE[dtype], 4 * REL_STATE[dtype], f"{what} S")
-    o2 = api.la_forward_gated(q, k, v, lg, scale, S)
-    assert torch.equal(o, o2)
+    o2, S2 = api.la_forward_gated(q, k, v, lg, scale, S, return_state=True)
+    assert torch.equal(o, o2) and torch.equal(S_out, S2)
+    close(api.la_forward_gated(q, k, v, lg, scale, S), ro, REL[dtype], MAX[dtype], f"{what} o alone")
 
 
 def check_bwd(dtype, ins, scale, state, what=""):
@@ -59,9 +60,12 @@ def check_bwd(dtype, ins, scale, state, what=""):
         close(g, r, REL[dtype], MAX[dtype], f"{what} {n}")
     close(got[3], ref[3], REL[dtype] * (4 if dtype == torch.float32 else 1), MAX[dtype], f"{what} dlog_gate")
     close(got[4], ref[4], REL_STATE[dtype], 4 * REL_STATE[dtype], f"{what} dS_in")
-    again = api.la_backward_gated(q, k, v, lg, dO, scale, S, dS)
+    again = api.la_backward_gated(q, k, v, lg, dO, scale, S, dS, return_dstate=True)
     for a, b in zip(got, again):
         assert torch.equal(a, b)
+    alone = api.la_backward_gated(q, k, v, lg, dO, scale, S, dS)
+    for n, g, r in zip(("dq", "dk", "dv"), alone, ref):
+        close(g, r, REL[dtype], MAX[dtype], f"{what} {n} alone")
 
 
 @pytest.mark.parametrize("shape", SHAPES)
