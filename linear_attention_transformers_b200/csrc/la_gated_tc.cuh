@@ -369,10 +369,10 @@ gated_span_kernel(const __grid_constant__ GatedSpanParams prm) {
 #pragma unroll
                 for (int i = 0; i < D / 16; ++i)
                     x[i] = *reinterpret_cast<const uint4*>(src + tile_chunk_off(C, row, q0 + i));
-                if (!(ok = __all_sync(0xffffffffu, blk == 0 || mbar_wait(sc_free, (blk - 1) & 1,
-                                                                         abort_flag))))
-                    break;
                 const float wr = w[(b % nbv) * C + row];
+                // the first part in place; the others wait for the products that
+                // still read the block before's
+                uint4 later[SPLIT - 1][D / 16];
 #pragma unroll
                 for (int i = 0; i < D / 16; ++i) {
                     const uint32_t raw[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
@@ -387,12 +387,20 @@ gated_span_kernel(const __grid_constant__ GatedSpanParams prm) {
                                 f = fma2(unpack_bf16(part[c][j]), make_float2(-1.f, -1.f), f);
                         }
                     }
-                    const uint32_t off = tile_chunk_off(C, row, q0 + i);
+                    *reinterpret_cast<uint4*>(src + tile_chunk_off(C, row, q0 + i)) =
+                        make_uint4(part[0][0], part[0][1], part[0][2], part[0][3]);
 #pragma unroll
-                    for (int c = 0; c < SPLIT; ++c)
-                        *reinterpret_cast<uint4*>((c == 0 ? src : lo + (c - 1) * Cfg::TILE) + off) =
+                    for (int c = 1; c < SPLIT; ++c)
+                        later[c - 1][i] =
                             make_uint4(part[c][0], part[c][1], part[c][2], part[c][3]);
                 }
+                if (!(ok = blk == 0 || warp_wait(sc_free, (blk - 1) & 1, abort_flag))) break;
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+                    for (int c = 0; c + 1 < SPLIT; ++c)
+                        *reinterpret_cast<uint4*>(lo + c * Cfg::TILE +
+                                                  tile_chunk_off(C, row, q0 + i)) = later[c][i];
                 fence_proxy_async_smem();
                 warp_arrive(sc_full);
             }
