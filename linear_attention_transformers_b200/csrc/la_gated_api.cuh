@@ -59,9 +59,13 @@ struct GatedTcPlan {
 // How the border states are formed: spans in parallel (0; two launches and the
 // float32 records) or a walk of CTAs of 64 or 32 value columns, whichever the
 // model below says is sooner, in us.  G: tiles a block (a group's query heads,
-// for R).  Measured (spans; walk with 64; with 32): 128 heads of 8192 tokens, D =
-// 64: 117, 97, 117; 64 of 4096, D = 128: 61, 54, 65; 32 of 131072, D = 128: 811,
-// 1435, 904; 8 of 777, D = 128: 20, 21, 15.
+// for R).  Measured for S, bf16 to the blocks only (spans; walk with 64; with
+// 32): 128 heads of 8192 tokens, D = 64: 118, 94, 122; 64 of 4096, D = 128,
+// single blocks: 89, 62, 79; 32 of 131072, D = 128: 763, 1326, 916; 8 of 777, D =
+// 128, single blocks: 20, 19, 15; 8 of 16384, D = 64: 38, 174, 138.  With a
+// float32 state for the caller 134, 104, 123 for the first.  For R with <S, R>,
+// in the same order: 183, 129, 158; 155, 81, 101; 29, 37, 27 (groups of 4); 78,
+// 239, 180.
 int pick_chain(int64_t kvh, int64_t nblk, int64_t D, int64_t G) {
     const double sms = num_sms(), tiles = double(nblk) * double(G);
     const double spans = 10.0 + double(kvh) * tiles * (D == 64 ? 0.0134 : 0.0243);
@@ -426,13 +430,9 @@ la_status run_gated_step(float* S, const void* q, const void* k, const void* v, 
     const T *tq = static_cast<const T*>(q), *tk = static_cast<const T*>(k),
             *tv = static_cast<const T*>(v), *tl = static_cast<const T*>(lg);
     la::LaunchScope scope("gated_step", st);
-    constexpr int DC = D / 4 < 16 ? 16 : D / 4;
-    if (kvh < 4 * num_sms())
-        la::gated_step_kernel<T, D, DC><<<unsigned(kvh * (D / DC)), 2 * D, 0, st>>>(
-            S, tq, tk, tv, tl, static_cast<T*>(o), G, scale);
-    else
-        la::gated_step_kernel<T, D, D><<<unsigned(kvh), 2 * D, 0, st>>>(
-            S, tq, tk, tv, tl, static_cast<T*>(o), G, scale);
+    constexpr int DC = la::gated_step_columns<D>;
+    la::gated_step_kernel<T, D, DC><<<unsigned(kvh * (D / DC)), 2 * D, 0, st>>>(
+        S, tq, tk, tv, tl, static_cast<T*>(o), G, scale);
     return launch_status();
 }
 

@@ -11,8 +11,8 @@
 //
 // What does not depend on each other shares a launch (the backward's four
 // gradients, the two directions of the states), since the sizes that come here
-// leave most SMs idle: B2 H6 Hkv2 N333 D64 float32, backward, 132 us in eight
-// launches.
+// leave most SMs idle: B2 H6 Hkv2 N333 D64 float32, backward, took 132 us in
+// eight launches and takes 66 in three.  B3 H6 N1000 D32 float32, forward: 26 us.
 //
 // All products are register-tiled float32 (4 rows x D/16 columns a thread)
 // from float32 tiles in shared memory, so nothing is rounded below float32;

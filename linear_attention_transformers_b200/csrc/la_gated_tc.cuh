@@ -48,10 +48,10 @@ struct alignas(16) GateTab {
 
 // MMAs issued by one lane of a warp that runs the issue loop together: the
 // descriptors stay warp-uniform values and only the instruction is predicated.
-// Inside `if (lane == 0)` the issuing thread needs more instructions an MMA
-// (131072 tokens, D = 128, forward blocks: 1554 us, 1368 this way on the same
-// GPU), and in gated_bwd64_kernel, with its many tiles, 180 cycles an MMA
-// against 45 to 60.
+// Inside `if (lane == 0)` the issuing thread needs more instructions an MMA: the
+// forward's blocks take 1029 us that way and 940 this way at 131072 tokens, 32
+// heads, D = 128, and 127 and 114 at B8 H16 N8192 D64; in gated_bwd_kernel, with
+// its many tiles, an MMA took 180 cycles to issue against 45 to 60.
 __device__ __forceinline__ void umma_one(uint32_t one, uint32_t d_tmem, uint64_t adesc,
                                          uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
@@ -91,9 +91,8 @@ __device__ __forceinline__ uint32_t elect_lane() {
         : "=r"(one));
     return one;
 }
-// One arrival for a warp, after what each of its lanes did before (an arrival by
-// every thread is an operation on one shared word each: 512 of them, several
-// times a block, kept the shared-memory pipe busy for a third of the block).
+// One arrival for a warp, after what each of its lanes did before (as fast as an
+// arrival by every thread, with 32 times fewer operations on shared memory).
 __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
     __syncwarp();
     if ((threadIdx.x & 31) == 0) sm100::mbar_arrive(bar);
@@ -530,6 +529,12 @@ struct GatedBlockCfg {
     static_assert(CTAS * T_COLS <= 512, "TMEM budget");
 };
 
+// Measured: B8 H16 N8192 D64 112 us (604 MB of tiles, states and output: 5.4 TB/s,
+// 0.83 of a copy's bandwidth; single blocks), 32 heads of 131072 tokens, D = 128,
+// 950 us (4.83 GB: 5.1 TB/s, 0.78; spans of two blocks).  Cores issue in half of
+// the cycles at most and the tensor pipe is busy in a quarter: what is left of the
+// bandwidth is the latency from P to its weights to the product that reads them.
+//
 // Warps: 0 TMA loads of the ring, 1 MMA, 2 gate tables and TMA loads of q, 3
 // TMA stores, from 4 on compute: NG groups of four warps, group h for 128 / NG
 // columns of every C x C product and D / NG of the output.
