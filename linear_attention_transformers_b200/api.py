@@ -623,9 +623,9 @@ def la_forward_gated(q, k, v, log_gate, scale: float = 1.0, S_in=None, o=None,
             S_out = torch.empty((B, Hkv, D, D), dtype=torch.float32, device=q.device)
         ws, ws_bytes = _scratch("la_forward_gated", lib.la_workspace_size_gated(
             LA_OP_FORWARD, B, H, Hkv, N, D, code), workspace, q.device)
-        st = lib.la_forward_gated(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_gate.data_ptr(), o.data_ptr(), _ptr(S_in),
-                                  _ptr(S_out), scale, B, H, Hkv, N, D, code, _ptr(ws),
-                                  ws_bytes, handle)
+        st = lib.la_forward_gated(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_gate.data_ptr(),
+                                  o.data_ptr(), _ptr(S_in), _ptr(S_out), scale, B, H, Hkv, N, D,
+                                  code, _ptr(ws), ws_bytes, handle)
     _check("la_forward_gated", st)
     return (o, S_out) if return_state else o
 
@@ -655,10 +655,10 @@ def la_backward_gated(q, k, v, log_gate, dO, scale: float = 1.0, S_in=None, dS_o
             dS_in = torch.empty((B, Hkv, D, D), dtype=torch.float32, device=q.device)
         ws, ws_bytes = _scratch("la_backward_gated", lib.la_workspace_size_gated(
             LA_OP_BACKWARD, B, H, Hkv, N, D, code), workspace, q.device)
-        st = lib.la_backward_gated(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_gate.data_ptr(), _ptr(dO),
-                                   _ptr(S_in), _ptr(dS_out), _ptr(dq), _ptr(dk), _ptr(dv),
-                                   _ptr(dlog_gate), _ptr(dS_in), scale, B, H, Hkv, N, D,
-                                   code, _ptr(ws), ws_bytes, handle)
+        st = lib.la_backward_gated(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_gate.data_ptr(),
+                                   _ptr(dO), _ptr(S_in), _ptr(dS_out), _ptr(dq), _ptr(dk), _ptr(dv),
+                                   _ptr(dlog_gate), _ptr(dS_in), scale, B, H, Hkv, N, D, code,
+                                   _ptr(ws), ws_bytes, handle)
     _check("la_backward_gated", st)
     return (dq, dk, dv, dlog_gate, dS_in) if return_dstate else (dq, dk, dv, dlog_gate)
 
@@ -674,8 +674,9 @@ def la_decode_step_gated(S, q, k, v, log_gate, scale: float = 1.0, o=None, strea
         _check_qkv("la_decode_step_gated", q, o)
     with _LaunchOn(q, stream) as handle:
         o = torch.empty_like(q) if o is None else o
-        st = lib.la_decode_step_gated(_ptr(S), q.data_ptr(), k.data_ptr(), v.data_ptr(), log_gate.data_ptr(), o.data_ptr(),
-                                      scale, B, H, Hkv, D, code, handle)
+        st = lib.la_decode_step_gated(_ptr(S), q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                                      log_gate.data_ptr(), o.data_ptr(), scale, B, H, Hkv, D, code,
+                                      handle)
     _check("la_decode_step_gated", st)
     return o
 
@@ -1063,7 +1064,10 @@ class LinearAttention(torch.autograd.Function):
 
 class GatedLinearAttention(torch.autograd.Function):
     """torch autograd wrapper of la_forward_gated / la_backward_gated: o, or
-    (o, S) with ``return_state``; gradients for q, k, v, log_gate and S_in."""
+    (o, S) with ``return_state``; gradients for q, k, v, log_gate and S_in
+    (of first order: differentiating them again raises).  To capture a backward
+    in a CUDA graph, first drop the autograd graphs of the same leaves that were
+    built outside the capture: torch would wait for their streams within it."""
 
     @staticmethod
     def forward(ctx, q, k, v, log_gate, scale=1.0, S_in=None, return_state=False):
@@ -1075,6 +1079,7 @@ class GatedLinearAttention(torch.autograd.Function):
         return la_forward_gated(q, k, v, log_gate, ctx.scale, S_in, return_state=return_state)
 
     @staticmethod
+    @torch.autograd.function.once_differentiable
     def backward(ctx, dO, dS_out=None):
         q, k, v, log_gate, S_in = ctx.saved_tensors
         if dO is None and dS_out is None:
@@ -1088,7 +1093,8 @@ class GatedLinearAttention(torch.autograd.Function):
 
 
 class HeadGroupNorm(torch.autograd.Function):
-    """torch autograd wrapper of la_group_norm / la_group_norm_backward."""
+    """torch autograd wrapper of la_group_norm / la_group_norm_backward
+    (gradients of first order: differentiating them again raises)."""
 
     @staticmethod
     def forward(ctx, x, weight, bias=None, gate=None, act="silu", eps=1e-5):
@@ -1100,6 +1106,7 @@ class HeadGroupNorm(torch.autograd.Function):
         return la_group_norm(x, weight, bias, gate, act, ctx.eps)
 
     @staticmethod
+    @torch.autograd.function.once_differentiable
     def backward(ctx, dy):
         x, weight, bias, gate = ctx.saved_tensors
         dx, dweight, dbias, dgate = la_group_norm_backward(x, weight, dy.contiguous(), bias, gate,

@@ -324,6 +324,18 @@ def test_autograd_leaves_what_is_not_asked():
     close(k.grad, ref[1], REL[torch.float32], MAX[torch.float32], "dk")
 
 
+def test_second_derivatives_raise():
+    q, k, v, lg, dO, *_ = tensors(1, 2, 2, 70, 32, torch.float32, 30)
+    q.requires_grad_()
+    o = api.GatedLinearAttention.apply(q, k, v, lg)
+    w = torch.ones(64, device="cuda")
+    y = api.HeadGroupNorm.apply(q, w)
+    for out in (o, y):
+        (dq,) = torch.autograd.grad(out.pow(2).sum(), q, create_graph=True)
+        with pytest.raises(RuntimeError):
+            dq.sum().backward()
+
+
 def test_refusals():
     q, k, v, lg, dO, S, dS = tensors(1, 4, 2, 32, 64, torch.bfloat16, 1)
     ok = (q, k, v, lg)
