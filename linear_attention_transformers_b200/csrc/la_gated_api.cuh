@@ -116,6 +116,15 @@ GatedTcPlan plan_gated_tc(la_op op, int64_t B, int64_t H, int64_t Hkv, int64_t N
 template <typename T, int D>
 constexpr bool gated_on_tensor_cores = std::is_same<T, __nv_bfloat16>::value && (D == 64 || D == 128);
 
+// A few tokens that no state enters or leaves, of at most a head an SM, run on
+// the plain cores in every type: one launch either way, no slower (8 heads,
+// forward and backward: 11 and 13 us, 12 and 15 on the tensor cores; 512 heads of
+// D = 128: 25 and 88, 19 and 31), and with so few products the one rounding of
+// each to bf16 would be most of the result's error.
+bool gated_few_tokens(int64_t B, int64_t H, int64_t N, bool states) {
+    return !states && N <= 16 && B * H <= num_sms();
+}
+
 // Sizes a gated launch can take: at most four blocks per 64 tokens of a head.
 la_status check_gated(int64_t B, int64_t H, int64_t Hkv, int64_t N, int64_t D, la_dtype dt) {
     la_status s;
@@ -535,11 +544,10 @@ la_status la_forward_gated(const void* q, const void* k, const void* v, const vo
         using T = decltype(t);
         constexpr int kD = decltype(d)::value;
         if constexpr (gated_on_tensor_cores<T, kD>)
-            return run_gated_fwd_tc<kD>(q, k, v, log_gate, o, S_in, S_out, scale, B, H, Hkv, N, ws,
-                                        st);
-        else
-            return run_gated_fwd<T, kD>(q, k, v, log_gate, o, S_in, S_out, scale, B, H, Hkv, N, ws,
-                                        st);
+            if (!gated_few_tokens(B, H, N, S_in || S_out))
+                return run_gated_fwd_tc<kD>(q, k, v, log_gate, o, S_in, S_out, scale, B, H, Hkv, N,
+                                            ws, st);
+        return run_gated_fwd<T, kD>(q, k, v, log_gate, o, S_in, S_out, scale, B, H, Hkv, N, ws, st);
     });
 }
 
@@ -578,11 +586,11 @@ la_status la_backward_gated(const void* q, const void* k, const void* v, const v
         using T = decltype(t);
         constexpr int kD = decltype(d)::value;
         if constexpr (gated_on_tensor_cores<T, kD>)
-            return run_gated_bwd_tc<kD>(q, k, v, log_gate, dO, S_in, dS_out, dq, dk, dv, dlog_gate,
-                                        dS_in, scale, B, H, Hkv, N, ws, st);
-        else
-            return run_gated_bwd<T, kD>(q, k, v, log_gate, dO, S_in, dS_out, dq, dk, dv, dlog_gate,
-                                        dS_in, scale, B, H, Hkv, N, ws, st);
+            if (!gated_few_tokens(B, H, N, S_in || dS_out || dS_in))
+                return run_gated_bwd_tc<kD>(q, k, v, log_gate, dO, S_in, dS_out, dq, dk, dv,
+                                            dlog_gate, dS_in, scale, B, H, Hkv, N, ws, st);
+        return run_gated_bwd<T, kD>(q, k, v, log_gate, dO, S_in, dS_out, dq, dk, dv, dlog_gate,
+                                    dS_in, scale, B, H, Hkv, N, ws, st);
     });
 }
 

@@ -1,6 +1,6 @@
 // la_gated_generic.cuh — gated linear attention on the plain cores, for every
-// type and head size (float32, and bf16 with D = 16 or 32, take it; see
-// la_gated_common.cuh for the formulas).  Chunks of 64 tokens, every chunk of
+// type and head size (float32, bf16 with D = 16 or 32, and calls of a few tokens
+// take it; see la_gated_common.cuh for the formulas).  Chunks of 64 tokens, every chunk of
 // every head a block of its own; the states at the chunks' borders are float32
 // records in the workspace:
 //
@@ -54,6 +54,12 @@ __device__ __forceinline__ void gated_load_tile(float* dst, const T* __restrict_
             *reinterpret_cast<float4*>(dst + r * LD + g * V + j) =
                 make_float4(f[j], f[j + 1], f[j + 2], f[j + 3]);
     }
+}
+
+// Tokens of the chunk from n0 on, up to a multiple of 4 (a thread's rows): what
+// the products go over.  A call of a few tokens takes a fraction of a chunk's time.
+__device__ __forceinline__ int gated_rows(int64_t n0, int64_t N) {
+    return N - n0 >= kGatedC ? kGatedC : (int(N - n0) + 3) & ~3;
 }
 
 // Inclusive sums of log2 gates of one chunk (0 past N); every thread may read
@@ -268,11 +274,12 @@ gated_carry_kernel(const GatedCarryJob fwd, const GatedCarryJob rev, int64_t tot
 
 // acc[r][c] += sum_e X[row r][e] Y[e][col c] with Y the record S (TRANS false,
 // Y[e][c] = S[e][c]) or its transpose (Y[e][c] = S[c][e]), 64 rows of Y at a
-// time through the shared tile `buf` ([64][D + 4] floats).
+// time through the shared tile `buf` ([64][D + 4] floats); rows from `rows` on
+// are left out.
 template <int D, bool TRANS>
 __device__ __forceinline__ void gated_mm_state(float (&acc)[4][D / 16], const float* X,
-                                               const float* __restrict__ S, float* buf, int ty,
-                                               int tx) {
+                                               const float* __restrict__ S, float* buf, int rows,
+                                               int ty, int tx) {
     constexpr int LD = GatedTile::ld(D);
     constexpr int KB = D < kGatedC ? D : kGatedC;
     for (int k0 = 0; k0 < D; k0 += KB) {
@@ -286,7 +293,7 @@ __device__ __forceinline__ void gated_mm_state(float (&acc)[4][D / 16], const fl
                 buf[a * LD + b] = S[(k0 + a) * D + b];
         }
         __syncthreads();
-        gated_mm_nn<D / 16>(acc, X + k0, LD, buf, LD, KB, ty, tx);
+        if (4 * ty < rows) gated_mm_nn<D / 16>(acc, X + k0, LD, buf, LD, KB, ty, tx);
     }
 }
 
@@ -314,6 +321,8 @@ __device__ __forceinline__ void gated_rows_block(
     const int64_t kvh = REV ? head : head / group;
     const int64_t n0 = int64_t(chunk) * kGatedC;
     const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
+    const int rows = gated_rows(n0, N);
+    const bool live = 4 * ty < rows;
     gated_load_gates(G, lg + kvh * N, n0, N);
     gated_load_tile<T, D>(tr, R + head * N * D, n0, N);
     float acc[4][NC] = {};
@@ -324,7 +333,7 @@ __device__ __forceinline__ void gated_rows_block(
         gated_load_tile<T, D>(tv, V + src, n0, N);
         __syncthreads();
         float p[4][4] = {};
-        gated_mm_nt<D, 4>(p, tr, LD, tk, LD, ty, tx);
+        if (live) gated_mm_nt<D, 4>(p, tr, LD, tk, LD, ty, tx);
 #pragma unroll
         for (int r = 0; r < 4; ++r)
 #pragma unroll
@@ -335,12 +344,13 @@ __device__ __forceinline__ void gated_rows_block(
                 tp[i * LP + j] = in ? in_mul * w * p[r][c] : 0.f;
             }
         __syncthreads();
-        gated_mm_nn<NC>(acc, tp, LP, tv, LD, kGatedC, ty, tx);
+        if (live) gated_mm_nn<NC>(acc, tp, LP, tv, LD, rows, ty, tx);
         __syncthreads();
     }
     if (rec) {
         float s[4][NC] = {};
-        gated_mm_state<D, TRANS>(s, tr, rec + (kvh * nchunk + chunk) * int64_t(D) * D, tk, ty, tx);
+        gated_mm_state<D, TRANS>(s, tr, rec + (kvh * nchunk + chunk) * int64_t(D) * D, tk, rows,
+                                 ty, tx);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
             const int i = 4 * ty + r;
@@ -383,6 +393,8 @@ __device__ __forceinline__ void gated_dgate_block(
     const int tid = threadIdx.x, ty = tid / 16, tx = tid % 16;
     const float* S = recS ? recS + (head * nchunk + chunk) * int64_t(D) * D : nullptr;
     const float* R = recR ? recR + (head * nchunk + chunk) * int64_t(D) * D : nullptr;
+    const int n_rows = gated_rows(n0, N);
+    const bool live = 4 * ty < n_rows;
     gated_load_gates(G, lg + head * N, n0, N);
     gated_load_tile<T, D>(tk, k + head * N * D, n0, N);
     gated_load_tile<T, D>(tv, v + head * N * D, n0, N);
@@ -394,8 +406,10 @@ __device__ __forceinline__ void gated_dgate_block(
         gated_load_tile<T, D>(tb, dO + src, n0, N);
         __syncthreads();
         float p[4][4] = {}, w[4][4] = {};
-        gated_mm_nt<D, 4>(p, ta, LD, tk, LD, ty, tx);
-        gated_mm_nt<D, 4>(w, tb, LD, tv, LD, ty, tx);
+        if (live) {
+            gated_mm_nt<D, 4>(p, ta, LD, tk, LD, ty, tx);
+            gated_mm_nt<D, 4>(w, tb, LD, tv, LD, ty, tx);
+        }
 #pragma unroll
         for (int r = 0; r < 4; ++r)
 #pragma unroll
@@ -411,7 +425,7 @@ __device__ __forceinline__ void gated_dgate_block(
             float s[4][NC] = {};
             // the state passes through no tile that is still read: k and v are
             // reloaded below
-            gated_mm_state<D, false>(s, ta, S, tk, ty, tx);
+            gated_mm_state<D, false>(s, ta, S, tk, n_rows, ty, tx);
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 const int i = 4 * ty + r;
@@ -436,7 +450,7 @@ __device__ __forceinline__ void gated_dgate_block(
     __syncthreads();
     if (R) {  // e^{G_C-G_j} k_j^T R v_j
         float s[4][NC] = {};
-        gated_mm_state<D, false>(s, tk, R, ta, ty, tx);
+        gated_mm_state<D, false>(s, tk, R, ta, n_rows, ty, tx);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
             const int j = 4 * ty + r;

@@ -110,6 +110,23 @@ def test_many_heads_and_long_ones(D, shape):
     close(plain, api.la_forward_gated(*wide[:4], 0.1).cpu(), REL[bf], MAX[bf], "o without a state")
 
 
+@pytest.mark.parametrize("shape", [(2, 4, 4, 1), (1, 6, 2, 2), (1, 1, 1, 5), (2, 8, 1, 16), (1, 148, 148, 3),
+                                   (1, 148, 37, 16)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_a_few_tokens_are_rounded_once(D, shape):
+    # bf16 in, float32 within, one rounding out: half a step of each value, and what
+    # float32 sums of D + 16 terms leave of the largest
+    B, H, Hkv, N = shape
+    ins = tensors(B, H, Hkv, N, D, torch.bfloat16, N + H, resets=True)
+    q, k, v, lg, dO, *_ = ins
+    scale = D ** -0.5
+    got = (api.la_forward_gated(q, k, v, lg, scale), *api.la_backward_gated(q, k, v, lg, dO, scale))
+    ref = (gated.forward(q, k, v, lg, scale)[0], *gated.backward(q, k, v, lg, dO, scale)[:4])
+    for n, g, r in zip(("o", "dq", "dk", "dv", "dlog_gate"), got, ref):
+        off = np.abs(g.double().cpu().numpy() - r)
+        assert (off <= 2.0 ** -8 * np.abs(r) + 2.0 ** -16 * np.abs(r).max()).all(), n
+
+
 @pytest.mark.parametrize("gate", [0.0, -1e-3, -5.0, -80.0, -300.0, -math.inf])
 @pytest.mark.parametrize("D", [32, 64, 128])
 @pytest.mark.parametrize("dtype", TYPES)
