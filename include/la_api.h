@@ -511,7 +511,8 @@ typedef enum la_act {
  * [B, N, H*D] (required exactly when gate is given), dweight float32 [H*D],
  * dbias float32 [H*D] (may be NULL).  The statistics are computed again from
  * x.  The channel sums are added in a fixed order.  Workspace:
- * la_workspace_size_group_norm.  N = 0 writes zeros to dweight and dbias.
+ * la_workspace_size_group_norm.  Without rows (B = 0 or N = 0) dweight and
+ * dbias are zeros.
  */
 LA_EXPORT la_status la_group_norm(const void *x, const void *gate, const float *weight,
                                   const float *bias, void *y, float eps, la_act act, int64_t B,

@@ -648,10 +648,10 @@ la_status la_group_norm_backward(const void* x, const void* gate, const float* w
         (s = check_opt(dbias)) || (s = check_opt(workspace)))
         return s;
     if ((gate == nullptr) != (dgate == nullptr)) return LA_ERR_INVALID_ARG;
-    if (B == 0 || H == 0) return LA_OK;
+    if (H == 0) return LA_OK;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if ((s = check_ptr(weight)) || (s = check_ptr(dweight))) return s;
-    if (N == 0) {  // no rows: the channel sums are empty
+    if (B == 0 || N == 0) {  // no rows: the channel sums are empty, and outputs still
         cudaError_t e = cudaMemsetAsync(dweight, 0, size_t(H * D) * 4, st);
         if (e == cudaSuccess && dbias) e = cudaMemsetAsync(dbias, 0, size_t(H * D) * 4, st);
         return e == cudaSuccess ? LA_OK : cuda_fail("la_group_norm_backward: zeros", e);

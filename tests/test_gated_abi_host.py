@@ -92,3 +92,13 @@ def test_norm_refusals(lib):
                                           None)
     assert back(gate=F) == INVALID and back(dgate=F) == INVALID and back(dw=None) == INVALID
     assert back(dx=None) == INVALID and back(ws=None) == WORKSPACE and back(n=8) == WORKSPACE
+
+
+def test_an_empty_batch_still_writes_the_channel_sums(lib):
+    # so their pointers are needed, as with N = 0; without channels nothing is
+    def back(B, H, N, w=F, dw=F):
+        return lib.la_group_norm_backward(None, None, w, None, None, None, None, dw, None, 1e-5, 1, B, H, N, 64, BF,
+                                          None, 0, None)
+    for B, N in ((0, 8), (0, 0), (1, 0)):
+        assert back(B, 2, N, dw=None) == INVALID and back(B, 2, N, w=None) == INVALID
+        assert back(B, 0, N, w=None, dw=None) == api.LA_OK

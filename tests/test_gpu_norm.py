@@ -113,3 +113,18 @@ def test_streams_and_refusals():
         api.la_group_norm_backward(x, w, dy, dbias=torch.empty_like(w))
     with pytest.raises(ValueError):
         api.la_group_norm_backward(x, w, dy.float())
+
+
+def test_an_empty_batch_has_channel_sums_of_zero():
+    # dweight and dbias have H*D elements whatever the batch is
+    for N in (0, 5):
+        x = torch.empty(0, 3, N, 64, device="cuda")
+        w = torch.ones(192, device="cuda")
+        e = torch.empty(0, N, 192, device="cuda")
+        dw, db = torch.full((2, 192), 7.0, device="cuda").unbind(0)
+        dx, dw2, db2, dg = api.la_group_norm_backward(x, w, e, bias=w, gate=e, dweight=dw, dbias=db)
+        assert dw2 is dw and db2 is db and not dw.any() and not db.any()
+        assert dx.shape == x.shape and dg.shape == e.shape
+        wg, bg = w.clone().requires_grad_(), w.clone().requires_grad_()
+        api.HeadGroupNorm.apply(x, wg, bg, e).sum().backward()
+        assert not wg.grad.any() and not bg.grad.any()
