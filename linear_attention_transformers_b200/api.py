@@ -584,6 +584,15 @@ def _check_like(name, what, t, ref, shape, dtype=None):
                          f"on {ref.device}")
 
 
+def _written(*given):
+    """Tells autograd which of the caller's own tensors a call wrote through their
+    pointers (fresh outputs are None here), so that a pending backward that saved
+    one raises instead of reading what has replaced it."""
+    given = [t for t in given if t is not None]
+    if given:
+        torch.autograd.graph.increment_version(given)
+
+
 def _scratch(name, need, workspace, device):
     if workspace is None:
         return (torch.empty(need, dtype=torch.uint8, device=device), need) if need else (None, 0)
@@ -616,6 +625,7 @@ def la_forward_gated(q, k, v, log_gate, scale: float = 1.0, S_in=None, o=None,
             _check_like("la_forward_gated", what, t, q, (B, Hkv, D, D), torch.float32)
     if o is not None:
         _check_qkv("la_forward_gated", q, o)
+    given = (o, S_out)
     with _LaunchOn(q, stream) as handle:
         if o is None:
             o = torch.empty_like(q)
@@ -626,6 +636,7 @@ def la_forward_gated(q, k, v, log_gate, scale: float = 1.0, S_in=None, o=None,
         st = lib.la_forward_gated(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_gate.data_ptr(),
                                   o.data_ptr(), _ptr(S_in), _ptr(S_out), scale, B, H, Hkv, N, D,
                                   code, _ptr(ws), ws_bytes, handle)
+    _written(*given)
     _check("la_forward_gated", st)
     return (o, S_out) if return_state else o
 
@@ -646,6 +657,7 @@ def la_backward_gated(q, k, v, log_gate, dO, scale: float = 1.0, S_in=None, dS_o
                                                                       log_gate)):
         if t is not None:
             _check_like("la_backward_gated", what, t, ref, ref.shape)
+    given = (dq, dk, dv, dlog_gate, dS_in)
     with _LaunchOn(q, stream) as handle:
         dq = torch.empty_like(q) if dq is None else dq
         dk = torch.empty_like(k) if dk is None else dk
@@ -659,6 +671,7 @@ def la_backward_gated(q, k, v, log_gate, dO, scale: float = 1.0, S_in=None, dS_o
                                    _ptr(dO), _ptr(S_in), _ptr(dS_out), _ptr(dq), _ptr(dk), _ptr(dv),
                                    _ptr(dlog_gate), _ptr(dS_in), scale, B, H, Hkv, N, D, code,
                                    _ptr(ws), ws_bytes, handle)
+    _written(*given)
     _check("la_backward_gated", st)
     return (dq, dk, dv, dlog_gate, dS_in) if return_dstate else (dq, dk, dv, dlog_gate)
 
@@ -672,11 +685,13 @@ def la_decode_step_gated(S, q, k, v, log_gate, scale: float = 1.0, o=None, strea
     _check_like("la_decode_step_gated", "S", S, q, (B, Hkv, D, D), torch.float32)
     if o is not None:
         _check_qkv("la_decode_step_gated", q, o)
+    given = (S, o)
     with _LaunchOn(q, stream) as handle:
         o = torch.empty_like(q) if o is None else o
         st = lib.la_decode_step_gated(_ptr(S), q.data_ptr(), k.data_ptr(), v.data_ptr(),
                                       log_gate.data_ptr(), o.data_ptr(), scale, B, H, Hkv, D, code,
                                       handle)
+    _written(*given)
     _check("la_decode_step_gated", st)
     return o
 
@@ -708,11 +723,13 @@ def la_group_norm(x, weight, bias=None, gate=None, act="silu", eps: float = 1e-5
     B, H, N, D = _check_norm("la_group_norm", x, weight, bias, gate, act)
     if y is not None:
         _check_like("la_group_norm", "y", y, x, (B, N, H * D))
+    given = y
     with _LaunchOn(x, stream) as handle:
         if y is None:
             y = torch.empty((B, N, H * D), dtype=x.dtype, device=x.device)
         st = lib.la_group_norm(_ptr(x), _ptr(gate), _ptr(weight), _ptr(bias), _ptr(y), eps,
                                ACT[act], B, H, N, D, DTYPE[x.dtype], handle)
+    _written(given)
     _check("la_group_norm", st)
     return y
 
@@ -732,6 +749,7 @@ def la_group_norm_backward(x, weight, dy, bias=None, gate=None, act="silu", eps:
                          ("dgate", dgate, dy)):
         if t is not None:
             _check_like("la_group_norm_backward", what, t, ref, ref.shape)
+    given = (dx, dweight, dbias, dgate)
     with _LaunchOn(x, stream) as handle:
         dx = torch.empty_like(x) if dx is None else dx
         dweight = torch.empty_like(weight) if dweight is None else dweight
@@ -745,6 +763,7 @@ def la_group_norm_backward(x, weight, dy, bias=None, gate=None, act="silu", eps:
                                         _ptr(dx), _ptr(dgate), _ptr(dweight), _ptr(dbias), eps,
                                         ACT[act], B, H, N, D, DTYPE[x.dtype], _ptr(ws), ws_bytes,
                                         handle)
+    _written(*given)
     _check("la_group_norm_backward", st)
     return dx, dweight, dbias, dgate
 
@@ -1067,7 +1086,10 @@ class GatedLinearAttention(torch.autograd.Function):
     (o, S) with ``return_state``; gradients for q, k, v, log_gate and S_in
     (of first order: differentiating them again raises).  To capture a backward
     in a CUDA graph, first drop the autograd graphs of the same leaves that were
-    built outside the capture: torch would wait for their streams within it."""
+    built outside the capture: torch would wait for their streams within it.
+    S_in is kept, not copied: when a call of this module has written it since (a
+    step in place, S_out, dS_in) the backward raises; a replayed graph's writes
+    are not seen."""
 
     @staticmethod
     def forward(ctx, q, k, v, log_gate, scale=1.0, S_in=None, return_state=False):

@@ -382,3 +382,48 @@ def test_refusals():
     with pytest.raises(ValueError):
         api.la_decode_step_gated(S[:, :1], q[:, :, 0].contiguous(), k[:, :, 0].contiguous(),
                                  v[:, :, 0].contiguous(), lg[:, :, 0].contiguous())
+
+
+def test_what_a_call_writes_is_known_to_autograd():
+    # the calls write through pointers; a tensor that a pending backward saved must
+    # not change unseen
+    q, k, v, lg, dO, S, dS = tensors(1, 4, 2, 70, 64, torch.bfloat16, 31)
+    at = [x[:, :, 0].contiguous() for x in (q, k, v, lg)]
+    q.requires_grad_()
+    plain = q.detach()
+
+    def stepped(S):
+        api.la_decode_step_gated(S, *at)
+
+    def returned(S):
+        api.la_forward_gated(plain, k, v, lg, S_out=S, return_state=True)
+
+    def differentiated(S):
+        api.la_backward_gated(plain, k, v, lg, dO, dS_out=dS, dS_in=S, return_dstate=True)
+
+    for write in (stepped, returned, differentiated):
+        state = S.clone()
+        o = api.GatedLinearAttention.apply(q, k, v, lg, 1.0, state)
+        write(state)
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            o.sum().backward()
+        # the state that a step leaves starts a pass of its own
+        api.GatedLinearAttention.apply(q, k, v, lg, 1.0, state).sum().backward()
+
+    def bumped(call, **outs):
+        before = {n: t._version for n, t in outs.items()}
+        call(**outs)
+        assert all(t._version > before[n] for n, t in outs.items()), outs.keys()
+
+    e = torch.empty_like
+    w = torch.ones(256, device="cuda")
+    y = torch.empty(1, 70, 256, dtype=plain.dtype, device="cuda")
+    gate = torch.randn_like(y)
+    bumped(lambda **t: api.la_forward_gated(plain, k, v, lg, **t), o=e(plain), S_out=e(S))
+    bumped(lambda **t: api.la_backward_gated(plain, k, v, lg, dO, **t), dq=e(plain), dk=e(k), dv=e(v),
+           dlog_gate=e(lg), dS_in=e(S))
+    bumped(lambda **t: api.la_decode_step_gated(q=at[0], k=at[1], v=at[2], log_gate=at[3], **t), S=S.clone(),
+           o=e(at[0]))
+    bumped(lambda **t: api.la_group_norm(plain, w, w, gate, **t), y=e(y))
+    bumped(lambda **t: api.la_group_norm_backward(plain, w, y.zero_(), w, gate, **t), dx=e(plain), dweight=e(w),
+           dbias=e(w), dgate=e(y))
