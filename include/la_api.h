@@ -447,7 +447,10 @@ LA_EXPORT la_status la_backward_sp_dkdv(const void *q, const void *k, const void
  * looked for; the state then grows as the recurrence says, until float32
  * overflows.  Sums of log gates are held in 64 bits, or in 32 counted from the
  * end that a weight is measured from.  A gate below 2^-126 may be taken as 0.
- * dlog_gate is the gradient with respect to log_gate (0 where the gate is 0).
+ * dlog_gate is the gradient with respect to log_gate, written as 0 where the
+ * gate is below 2^-126; it is the sum of what passes the gate, formed as a
+ * difference of float32 sums over the 128 tokens around it, so where hardly
+ * anything passes what it holds is the rounding of those sums.
  *
  * la_backward_gated: gradients of sum(dO * O) + sum(dS_out * S_out) with
  * respect to q, k, v, log_gate and S_in (dS_in, may be NULL).  dS_out may be

@@ -389,9 +389,15 @@ gated_bwd_kernel(const __grid_constant__ GatedBwdParams prm) {
             }
             const int64_t n0 = int64_t(blk_of(it)) * C + 4 * lane;
             __nv_bfloat16* out = prm.dlg + int64_t(head_of(it)) * prm.N;
+            // the gates once more, as differences of their sums in the table
+            const float4 l4 = *reinterpret_cast<const float4*>(&tabs[m & 1].loc[4 * lane]);
+            const float up = __shfl_up_sync(0xffffffffu, l4.w, 1);
+            const float l[5] = {lane % 8 ? up : 0.f, l4.x, l4.y, l4.z, l4.w};
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                if (n0 + j < prm.N) out[n0 + j] = __float2bfloat16_rn(gr[j]);
+                if (n0 + j < prm.N)
+                    out[n0 + j] =
+                        __float2bfloat16_rn(gate_is_zero(l[j + 1] - l[j]) ? 0.f : gr[j]);
         }
     } else if (warp == 3) {
         if (lane == 0) {

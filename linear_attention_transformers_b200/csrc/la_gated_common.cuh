@@ -45,6 +45,11 @@ __device__ __forceinline__ double gate_log2(float lg) {
     return x < -160.0 ? -160.0 : x;
 }
 
+// A gate below 2^-126, the least that float32 holds in full (NaN is not): its
+// gradient is written as 0.  What the sums over pairs and states would leave
+// there is their float32 rounding.
+__device__ __forceinline__ bool gate_is_zero(double log2_gate) { return log2_gate < -126.0; }
+
 __device__ __forceinline__ double warp_scan_sum(double x, int lane) {
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {

@@ -427,3 +427,22 @@ def test_what_a_call_writes_is_known_to_autograd():
     bumped(lambda **t: api.la_group_norm(plain, w, w, gate, **t), y=e(y))
     bumped(lambda **t: api.la_group_norm_backward(plain, w, y.zero_(), w, gate, **t), dx=e(plain), dweight=e(w),
            dbias=e(w), dgate=e(y))
+
+
+@pytest.mark.parametrize("N", [13, 64, 300, 1500])
+@pytest.mark.parametrize("D", [16, 64, 128])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_a_gate_of_zero_has_no_gradient(dtype, D, N):
+    # single gates of zero among gates near 1: nothing passes them, so their
+    # gradient is 0, not what rounding leaves of the pairs around them
+    for state in (False, True):
+        q, k, v, lg, dO, S, dS = tensors(1, 4, 2, N, D, dtype, 37 + N, gate=-0.01)
+        at = [0, 1, N // 3, N // 2, N // 2 + 1, N - 1]
+        lg[:, 0, at] = -math.inf
+        lg[:, 1, at[2:5]] = torch.tensor([-1000.0, -200.0, -88.0], dtype=dtype, device="cuda")  # below 2^-126
+        S, dS = (S, dS) if state else (None, None)
+        got = api.la_backward_gated(q, k, v, lg, dO, 0.3, S, dS)
+        ref = gated.backward(q, k, v, lg, dO, 0.3, S, dS)[3]
+        assert not got[3][:, 0, at].any() and not got[3][:, 1, at[2:5]].any()
+        ref[:, 1, at[2:5]] = 0.0
+        close(got[3], ref, REL[dtype] * (4 if dtype == torch.float32 else 1), MAX[dtype], "dlog_gate")
