@@ -468,6 +468,21 @@ gated_bwd_kernel(const __grid_constant__ GatedBwdParams prm) {
             }
             return dot.x + dot.y;
         };
+        // One step of the sums of columns over a warp's rows: of 2 n columns the lanes
+        // with bit `off` keep the last n, the others the first.  M stays float32: the
+        // first step is taken while its 16 columns are formed, so that half as many
+        // registers hold it until the products run.  After steps of 16, 8, 4 and 2 for
+        // each half of the 32 columns and one of 1 between the halves, lane l has the
+        // sum of column 16 (l % 2) + l / 2.
+        auto fold = [&](float* x, int n, int off) {
+            const bool up = (lane & off) != 0;
+#pragma unroll
+            for (int t = 0; t < n; ++t) {
+                const float give = up ? x[t] : x[t + n];
+                const float keep = up ? x[t + n] : x[t];
+                x[t] = keep + __shfl_xor_sync(0xffffffffu, give, off);
+            }
+        };
         auto put = [&](int t_acc, uint8_t* tile) {
 #pragma unroll
             for (int s = 0; s < GC / 16; ++s) {
@@ -490,7 +505,8 @@ gated_bwd_kernel(const __grid_constant__ GatedBwdParams prm) {
             for (int g = 0; g < G; ++g, ++u) {
                 if (!(ok = wait(pw_raw, u & 1))) break;
                 tc_fence_after();
-                uint32_t mp[16], pp[16], wp[16];  // M, P~, W~ in bf16 pairs
+                float mm[16];             // M, folded once: see fold
+                uint32_t pp[16], wp[16];  // P~, W~ in bf16 pairs
 #pragma unroll
                 for (int s = 0; s < 2; ++s) {
                     float pv[16], wv[16], ms[16];
@@ -533,10 +549,16 @@ gated_bwd_kernel(const __grid_constant__ GatedBwdParams prm) {
                     }
 #pragma unroll
                     for (int t = 0; t < 8; ++t) {
-                        mp[8 * s + t] = pack_bf16(ms[2 * t], ms[2 * t + 1]);
                         pp[8 * s + t] = pack_bf16(pv[2 * t], pv[2 * t + 1]);
                         wp[8 * s + t] = pack_bf16(wv[2 * t], wv[2 * t + 1]);
                     }
+                    if (J <= sp) {
+#pragma unroll
+                        for (int t = 0; t < 16; ++t) rsum += ms[t];
+                        fold(ms, 8, 16);
+                    }
+#pragma unroll
+                    for (int t = 0; t < 8; ++t) mm[8 * s + t] = ms[t];
                 }
                 tc_fence_before();
                 warp_arrive(p_read);
@@ -569,28 +591,15 @@ gated_bwd_kernel(const __grid_constant__ GatedBwdParams prm) {
                 fence_proxy_async_smem();
                 tc_fence_before();
                 warp_arrive(pw_full);
-                if (J <= sp) {  // M's sums while the products run
-                    // rows and columns add the same rounded values, so what cancels
-                    // between them still does
-                    float mm[32], rs = 0.f;
+                if (J <= sp) {  // the rest of M's column sums while the products run
 #pragma unroll
-                    for (int t = 0; t < 16; ++t) {
-                        const float2 f = unpack_bf16(mp[t]);
-                        mm[2 * t] = f.x;
-                        mm[2 * t + 1] = f.y;
-                        rs += f.x + f.y;
+                    for (int s = 0; s < 2; ++s) {
+                        fold(mm + 8 * s, 4, 8);
+                        fold(mm + 8 * s, 2, 4);
+                        fold(mm + 8 * s, 1, 2);
                     }
-                    rsum += rs;
-                    // lane l ends with the sum of column l over the warp's rows
-#pragma unroll
-                    for (int off = 16; off > 0; off >>= 1)
-#pragma unroll
-                        for (int t = 0; t < off; ++t) {
-                            const bool up = (lane & off) != 0;
-                            const float give = up ? mm[t] : mm[t + off];
-                            const float keep = up ? mm[t + off] : mm[t];
-                            mm[t] = keep + __shfl_xor_sync(0xffffffffu, give, off);
-                        }
+                    mm[1] = mm[8];
+                    fold(mm, 1, 1);
                     csum += mm[0];
                 }
                 // staged over the tiles that nothing reads any more; the store warp is
@@ -614,7 +623,7 @@ gated_bwd_kernel(const __grid_constant__ GatedBwdParams prm) {
                                   wait(&kv_free[(m - 1) % NB], ((m - 1) / NB) & 1))))
                 break;
             red[grp * C + irow] = rsum;
-            red[(4 + sp) * C + c0 + lane] = csum;
+            red[(4 + sp) * C + c0 + 16 * (lane & 1) + (lane >> 1)] = csum;
             red[(8 + grp) * C + irow] = through;
             fence_proxy_async_smem();
             tc_fence_before();

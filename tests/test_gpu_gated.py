@@ -446,3 +446,23 @@ def test_a_gate_of_zero_has_no_gradient(dtype, D, N):
         assert not got[3][:, 0, at].any() and not got[3][:, 1, at[2:5]].any()
         ref[:, 1, at[2:5]] = 0.0
         close(got[3], ref, REL[dtype] * (4 if dtype == torch.float32 else 1), MAX[dtype], "dlog_gate")
+
+
+@pytest.mark.parametrize("shape", [(1, 2, 2, 17), (2, 3, 3, 64), (1, 4, 2, 100), (3, 8, 1, 128)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_the_gates_gradient_inside_a_block_is_rounded_once(D, shape):
+    # a block that no state enters or leaves.  The terms of dlog_gate are products of
+    # float32 sums of exact products (2^-22 in all) and of weights whose exponents are
+    # differences of sums up to 64, each rounded to float32 (2^-19 off at most, two of
+    # them: 2^-18.5 of the weight) under an exponential good to 2^-22.  They are held and
+    # added in float32; a partial sum is no larger than the largest output by more than
+    # a few times, so 256 additions leave 16 * 2^-24.  Errors of independent terms add
+    # like the terms themselves: 2^-18 and a little of the largest value, 2^-16 is four
+    # times that, beside the half step of the output's own bf16
+    B, H, Hkv, N = shape
+    q, k, v, lg, dO, *_ = tensors(B, H, Hkv, N, D, torch.bfloat16, 41 + N)
+    got = api.la_backward_gated(q, k, v, lg, dO, D ** -0.5)[3].double().cpu().numpy()
+    ref = gated.backward(q, k, v, lg, dO, D ** -0.5)[3]
+    off = np.abs(got - ref)
+    assert (off <= 2.0 ** -8 * np.abs(ref) + 2.0 ** -16 * np.abs(ref).max()).all(), (
+        off / np.abs(ref).max()).max()
