@@ -213,7 +213,9 @@ la_status gated_tc_chain(const void* A, const void* Bm, const void* lg, const Ga
     prm.blocks = last ? prm.nblk : REV ? std::max(0, prm.nblk - p.nb) : (p.nspan - 1) * p.nb;
     auto kern = la::gated_chain_kernel<D, EC, REV, SPLIT>;
     if ((s = allow_smem(kern, Cfg::SMEM)) != LA_OK) return s;
-    la::LaunchScope scope(REV ? "gated_chain_rev" : "gated_chain", st);
+    la::LaunchScope scope(EC == 64 ? (REV ? "gated_chain64_rev" : "gated_chain64")
+                                   : (REV ? "gated_chain32_rev" : "gated_chain32"),
+                          st);
     kern<<<unsigned(kvh * (D / EC)), la::kGatedChainThreads, Cfg::SMEM, st>>>(prm);
     return launch_status();
 }
