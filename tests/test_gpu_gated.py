@@ -466,3 +466,52 @@ def test_the_gates_gradient_inside_a_block_is_rounded_once(D, shape):
     off = np.abs(got - ref)
     assert (off <= 2.0 ** -8 * np.abs(ref) + 2.0 ** -16 * np.abs(ref).max()).all(), (
         off / np.abs(ref).max()).max()
+
+
+@pytest.mark.parametrize("D", [32, 64])
+def test_autograd_takes_any_strides(D):
+    # transposed inputs, a sliced gate, a state and gradients that are expanded give
+    # what their contiguous copies give
+    q, k, v, lg, _, S, _ = tensors(2, 4, 2, 150, D, torch.bfloat16, 43)
+    far = [x.transpose(1, 2).contiguous().transpose(1, 2).requires_grad_() for x in (q, k, v)]
+    gate = torch.stack([lg, lg], -1)[..., 0].detach().requires_grad_()
+    start = S[:1].expand(2, -1, -1, -1).detach().requires_grad_()
+    assert not any(t.is_contiguous() for t in (*far, gate, start))
+    o, S_out = api.GatedLinearAttention.apply(*far, gate, 0.5, start, True)
+    S = S[:1].repeat(2, 1, 1, 1)
+    want = api.la_forward_gated(q, k, v, lg, 0.5, S, return_state=True)
+    assert torch.equal(o, want[0]) and torch.equal(S_out, want[1])
+    dO = torch.full((), 0.25, dtype=o.dtype, device="cuda").expand_as(o)
+    dS = torch.full((), 0.125, device="cuda").expand_as(S_out)
+    torch.autograd.backward([o, S_out], [dO, dS])
+    want = api.la_backward_gated(q, k, v, lg, dO.contiguous(), 0.5, S, dS.contiguous(), return_dstate=True)
+    for t, r in zip((*far, gate, start), want):
+        assert torch.equal(t.grad, r)
+
+
+def test_two_host_threads():
+    # each on a stream of its own, all calls at once
+    from concurrent.futures import ThreadPoolExecutor
+
+    def work(ins, stream=None):
+        q, k, v, lg, dO, S, dS = ins
+        with torch.cuda.stream(stream or torch.cuda.current_stream()):
+            w = torch.ones(q.shape[1] * q.shape[3], device="cuda")
+            o, S_out = api.la_forward_gated(q, k, v, lg, 0.5, S, return_state=True)
+            y = api.la_group_norm(o, w)
+            g = api.la_backward_gated(q, k, v, lg, dO, 0.5, S, dS, return_dstate=True)
+            s = api.la_decode_step_gated(S_out, *(x[:, :, 0].contiguous() for x in (q, k, v, lg)))
+        return (o, y, *g, s, S_out)
+
+    ins = [tensors(2, 4, 2, 700, D, torch.bfloat16, D) for D in (64, 128)]
+    want = [work(x) for x in ins]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in ins]
+    with ThreadPoolExecutor(2) as pool:
+        got = [pool.submit(lambda a, s: [work(a, s) for _ in range(20)], *p) for p in zip(ins, streams)]
+        got = [f.result() for f in got]
+    torch.cuda.synchronize()
+    api.la_get_device_error()
+    for runs, ref in zip(got, want):
+        for outs in runs:
+            assert all(torch.equal(a, b) for a, b in zip(outs, ref))

@@ -128,3 +128,51 @@ def test_an_empty_batch_has_channel_sums_of_zero():
         wg, bg = w.clone().requires_grad_(), w.clone().requires_grad_()
         api.HeadGroupNorm.apply(x, wg, bg, e).sum().backward()
         assert not wg.grad.any() and not bg.grad.any()
+
+
+def test_backward_on_another_stream_and_captured():
+    x, w, b, gate, dy = tensors(2, 4, 500, 64, torch.bfloat16, 10)
+    want = api.la_group_norm_backward(x, w, dy, b, gate)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    got = api.la_group_norm_backward(x, w, dy, b, gate, stream=s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(g, r) for g, r in zip(got, want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = api.la_group_norm_backward(x, w, dy, b, gate)
+    for seed in (10, 11):
+        for t, n in zip((x, w, b, gate, dy), tensors(2, 4, 500, 64, torch.bfloat16, seed)):
+            t.copy_(n)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(g, r) for g, r in zip(outs, api.la_group_norm_backward(x, w, dy, b, gate)))
+
+
+def test_long_offsets_backward():
+    # more than 2^31 elements: the last rows' dx and dgate equal a call's on them alone
+    H, N, D = 64, (1 << 31) // (64 * 128) + 5, 128
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.randn(1, H, N, D, generator=g, device="cuda", dtype=torch.bfloat16)
+    gate = torch.randn(1, N, H * D, generator=g, device="cuda", dtype=torch.bfloat16)
+    w = torch.ones(H * D, device="cuda")
+    dx, _, _, dg = api.la_group_norm_backward(x, w, gate, gate=gate)
+    tail = gate[:, -7:].contiguous()
+    dx2, _, _, dg2 = api.la_group_norm_backward(x[:, :, -7:].contiguous(), w, tail, gate=tail)
+    assert torch.equal(dx[:, :, -7:], dx2) and torch.equal(dg[:, -7:], dg2)
+
+
+def test_autograd_takes_any_strides():
+    # a transposed input, a sliced gate and an expanded gradient give what their
+    # contiguous copies give
+    x, w, b, gate, _ = tensors(2, 4, 50, 64, torch.bfloat16, 12)
+    far = x.transpose(1, 2).contiguous().transpose(1, 2).requires_grad_()
+    wide = torch.cat([gate, gate], -1)[..., :256].detach().requires_grad_()
+    wg, bg = w.clone().requires_grad_(), b.clone().requires_grad_()
+    y = api.HeadGroupNorm.apply(far, wg, bg, wide)
+    assert torch.equal(y, api.la_group_norm(x, w, b, gate))
+    dy = torch.full((1, 1, 1), 0.5, dtype=y.dtype, device="cuda").expand_as(y)
+    y.backward(dy)
+    want = api.la_group_norm_backward(x, w, dy.contiguous(), b, gate)
+    for got, ref in zip((far.grad, wg.grad, bg.grad, wide.grad), want):
+        assert torch.equal(got, ref)
