@@ -29,8 +29,8 @@
 // blocks' number times that latency, at about half of a copy's bandwidth.
 #pragma once
 
+#include "la_async_copy.cuh"
 #include "la_gated_tc.cuh"
-#include "la_norm.cuh"
 
 namespace la {
 

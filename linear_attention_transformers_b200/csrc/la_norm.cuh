@@ -23,6 +23,7 @@
 // the activation leave too few registers to keep enough bytes in flight.
 #pragma once
 
+#include "la_async_copy.cuh"
 #include "la_common.cuh"
 
 namespace la {
@@ -78,14 +79,6 @@ __device__ __forceinline__ float row_sum(float x) {
 #pragma unroll
     for (int o = LPR / 2; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
     return x;
-}
-
-// 16 bytes to shared memory, asynchronously; zeros where !ok
-__device__ __forceinline__ void copy16_async(void* dst, const void* src, bool ok) {
-    const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src),
-                 "r"(ok ? 16 : 0)
-                 : "memory");
 }
 
 // A token's place in x: offsets (in 16-byte groups) of one head's row, advanced
