@@ -445,8 +445,11 @@ LA_EXPORT la_status la_backward_sp_dkdv(const void *q, const void *k, const void
  * log_gate is the natural logarithm of a gate in [0, 1]: at most 0, and -inf
  * drops the state (a packed document's first token).  Values above 0 are not
  * looked for; the state then grows as the recurrence says, until float32
- * overflows.  Sums of log gates are held in 64 bits, or in 32 counted from the
- * end that a weight is measured from.  A gate below 2^-126 may be taken as 0.
+ * overflows.  Sums of log gates are held in 64 bits, or in 32 over at most 128
+ * tokens from the end that a weight is measured from, and in the bf16 kernels
+ * (D = 64, 128) between tokens of the same 32, from the start of those: a weight
+ * is then off by at most 2^-23 of the sum.  A gate below 2^-126 may be taken as 0
+ * (it counts as 2^-160 in the sums).
  * dlog_gate is the gradient with respect to log_gate, written as 0 where the
  * gate is below 2^-126; it is the sum of what passes the gate, formed as a
  * difference of float32 sums over the 128 tokens around it, so where hardly
@@ -460,13 +463,26 @@ LA_EXPORT la_status la_backward_sp_dkdv(const void *q, const void *k, const void
  *
  * Inputs are finite: a value that is not (a product of two that overflows
  * float32 among them) may reach every output of its 128 tokens, those before it
- * included, and every later one.
+ * included, and every later one; in the backward every earlier one too.  A gate
+ * of 0 does not hold it up.
  *
- * Types and sizes as la_forward's.  bf16 inputs are read exactly; the state
- * and all sums are float32.  Workspace: la_workspace_size_gated (0 for
- * arguments that the calls refuse); two calls that may overlap (two streams,
- * two captured graphs) need one each.  N = 0 copies S_in to S_out, and dS_out
- * to dS_in.  Errors as la_forward.
+ * Types and sizes as la_forward's.  bf16 inputs are read exactly; S_in, S_out,
+ * dS_out and dS_in are float32 and so are all sums.  With bf16 and D = 64 or 128
+ * the states at the borders of blocks and the weighted products of a block are
+ * rounded to bf16 once, as operands (up to 16 tokens of few heads without states
+ * are not).  How the states are formed goes by the number of heads and the length,
+ * so the last bits of a sequence's outputs may depend on the batch that it is in,
+ * and on whether a state is asked for.
+ *
+ * Workspace: la_workspace_size_gated (0 for arguments that the calls refuse); two
+ * calls that may overlap (two streams, two captured graphs) need one each.  It
+ * holds the border states: a backward with bf16 and D = 64 or 128 takes 4 D^2 to 8
+ * D^2 bytes per 128 tokens and key/value head (at D = 128 twice to four times the
+ * bytes of k; 4.3 GB for 32 heads of 131072 tokens), a forward at most 6 D^2 (D =
+ * 128: per 256 tokens); float32 and the other sizes 4 D^2 bytes per 64 tokens
+ * forward, 8 D^2 backward.
+ *
+ * N = 0 copies S_in to S_out, and dS_out to dS_in.  Errors as la_forward.
  */
 LA_EXPORT size_t la_workspace_size_gated(la_op op, int64_t B, int64_t H, int64_t Hkv, int64_t N,
                                          int64_t D, la_dtype dt);

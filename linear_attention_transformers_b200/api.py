@@ -614,7 +614,9 @@ def la_forward_gated(q, k, v, log_gate, scale: float = 1.0, S_in=None, o=None,
     """o = scale S_t^T q_t for S_t = exp(log_gate_t) S_{t-1} + k_t v_t^T.
 
     q [B, H, N, D]; k, v [B, Hkv, N, D]; log_gate [B, Hkv, N], at most 0 (-inf
-    drops the state), of q's dtype.  ``S_in``: the float32 state [B, Hkv, D, D]
+    drops the state), of q's dtype: one that autocast or a layer left in float32
+    is cast by the caller (to bfloat16 it moves a head's memory, 1 / -log_gate
+    tokens, by at most 2^-8 of itself), and the calls refuse it otherwise.  ``S_in``: the float32 state [B, Hkv, D, D]
     before the first token (None: zero).  ``return_state``: also return the
     state after the last token, in ``S_out`` if given.
     """

@@ -17,8 +17,9 @@ constexpr int64_t kMaxBlocks = (int64_t(1) << 31) - 1;
 // ------------------------------------------------------------------ the plan
 // Records of D*D float32 per key/value head and 64-token chunk: the state
 // entering each chunk (S), and for the backward the gradient of the state
-// leaving it (R), each with its chunks' gate products.  A head of one chunk
-// with neither state given needs none.
+// leaving it (R), each with its chunks' gate products.  A head of one chunk with
+// neither state given leaves them unused; they are reserved all the same, since
+// the size is asked for without saying which states are given.
 struct GatedPlan {
     int64_t nchunk = 0;
     size_t rec_bytes = 0, tot_bytes = 0;
@@ -117,10 +118,13 @@ template <typename T, int D>
 constexpr bool gated_on_tensor_cores = std::is_same<T, __nv_bfloat16>::value && (D == 64 || D == 128);
 
 // A few tokens that no state enters or leaves, of at most a head an SM, run on
-// the plain cores in every type: one launch either way, no slower (8 heads,
-// forward and backward: 11 and 13 us, 12 and 15 on the tensor cores; 512 heads of
-// D = 128: 25 and 88, 19 and 31), and with so few products the one rounding of
-// each to bf16 would be most of the result's error.
+// the plain cores in every type, so that a call of so few products is rounded
+// once; a token more, a head more or a state, and the products and states are
+// operands in bf16 again.  The kernels' times there, 16 tokens on the plain cores
+// and 17 on the tensor cores, us: forward D = 64 with 1, 37 and 148 heads 4.7, 5.0,
+// 5.1 and 6.5, 6.6, 7.4; D = 128: 6.4, 6.6, 6.6 and 6.8, 6.9, 7.5.  Backward, whose
+// blocks are four a head: D = 64 6.6, 6.6, 14.1 and 7.6, 7.7, 8.1; D = 128: 9.3, 9.0,
+// 28.9 and 8.3, 8.4, 9.0: above a block an SM it costs time for its rounding.
 bool gated_few_tokens(int64_t B, int64_t H, int64_t N, bool states) {
     return !states && N <= 16 && B * H <= num_sms();
 }

@@ -44,9 +44,11 @@ struct NormParams {
     float eps;
 };
 
-// bf16 tensors take the hardware's base-2 exponential and reciprocal (each
-// within 2^-21 of the value, rounded away right after); an exponential that
-// overflows gives 1 / inf = 0.
+// bf16 tensors take the hardware's base-2 exponential and reciprocal: with the
+// rounding of the exponent 2^-19 of the value for |x| up to 16, far below the half
+// step of the bf16 outputs (2^-8).  The float32 sums for weight and bias take it
+// too: over many tokens its errors add up as the terms do.
+// An exponential that overflows gives 1 / inf = 0.
 template <bool EXACT>
 __device__ __forceinline__ float norm_sigmoid(float x) {
     if (EXACT) return 1.f / (1.f + expf(-x));
