@@ -28,8 +28,8 @@
 //
 // Separate passes for dq, dk and dv read the four tensors again for each and left
 // dlog_gate's pieces to a fourth kernel: 656 us at B8 H16 N8192 D64 and 322 us at
-// B4 H16 N4096 D128, where this kernel takes 285 and 148 us.  It moves 1.07 GB and
-// 0.60 GB (3.8 and 4.1 TB/s, 0.58 and 0.62 of a copy's bandwidth).  D = 64: the
+// B4 H16 N4096 D128, where this kernel takes 299 and 143 us.  It moves 1.07 GB and
+// 0.60 GB (3.6 and 4.2 TB/s, 0.55 and 0.64 of a copy's bandwidth).  D = 64: the
 // warps of rows 96 to 127, which have most of the triangle, issue almost without
 // pause, and pack, product and epilogue of a block follow each other.  D = 128: one
 // block's tiles at a time (the next block's are brought to L2 ahead).

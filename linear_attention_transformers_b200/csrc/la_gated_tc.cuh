@@ -537,7 +537,8 @@ struct GatedBlockCfg {
 
 // Measured: B8 H16 N8192 D64 112 us (604 MB of tiles, states and output: 5.4 TB/s,
 // 0.83 of a copy's bandwidth; single blocks), 32 heads of 131072 tokens, D = 128,
-// 950 us (4.83 GB: 5.1 TB/s, 0.78; spans of two blocks).  Cores issue in half of
+// 950 us in a short run (4.83 GB: 5.1 TB/s, 0.78; spans of two blocks), 1043 to 1094
+// in one of a hundred milliseconds and more.  Cores issue in half of
 // the cycles at most and the tensor pipe is busy in a quarter: what is left of the
 // bandwidth is the latency from P to its weights to the product that reads them.
 //
