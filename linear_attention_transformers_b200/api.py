@@ -614,11 +614,12 @@ def la_forward_gated(q, k, v, log_gate, scale: float = 1.0, S_in=None, o=None,
     """o = scale S_t^T q_t for S_t = exp(log_gate_t) S_{t-1} + k_t v_t^T.
 
     q [B, H, N, D]; k, v [B, Hkv, N, D]; log_gate [B, Hkv, N], at most 0 (-inf
-    drops the state), of q's dtype: one that autocast or a layer left in float32
-    is cast by the caller (to bfloat16 it moves a head's memory, 1 / -log_gate
-    tokens, by at most 2^-8 of itself), and the calls refuse it otherwise.  ``S_in``: the float32 state [B, Hkv, D, D]
-    before the first token (None: zero).  ``return_state``: also return the
-    state after the last token, in ``S_out`` if given.
+    drops the state).  All of q's dtype: a log_gate that autocast or a layer left
+    in float32 beside bfloat16 q is refused; the caller casts it, which moves a
+    head's memory of 1 / -log_gate tokens by at most 2^-8 of itself.  ``S_in``: the
+    float32 state [B, Hkv, D, D] before the first token (None: zero).
+    ``return_state``: also return the state after the last token, in ``S_out`` if
+    given.
     """
     lib = load_library()
     B, H, Hkv, N, D, code = _check_gated("la_forward_gated", q, k, v, log_gate, 4)
@@ -1089,8 +1090,8 @@ class GatedLinearAttention(torch.autograd.Function):
     (of first order: differentiating them again raises).  To capture a backward
     in a CUDA graph, first drop the autograd graphs of the same leaves that were
     built outside the capture: torch would wait for their streams within it.
-    S_in is kept, not copied: when a call of this module has written it since (a
-    step in place, S_out, dS_in) the backward raises; a replayed graph's writes
+    S_in is kept, not copied: when a gated call has written it since (a step in
+    place, S_out, dS_in) the backward raises; a replayed graph's writes
     are not seen."""
 
     @staticmethod

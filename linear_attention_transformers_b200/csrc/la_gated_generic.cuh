@@ -500,8 +500,9 @@ __device__ __forceinline__ void gated_dgate_block(
         if (tid == 31) behind = 0.f;
         const int64_t n = n0 + 2 * tid;
         auto put = [&](int64_t at, float x) {
-            if (at < N)
-                dlg[head * N + at] = from_f32<T>(gate_is_zero(gate_log2(to_f32(lg[head * N + at]))) ? 0.f : x);
+            if (at >= N) return;
+            const double gate = gate_log2(to_f32(lg[head * N + at]));
+            dlg[head * N + at] = from_f32<T>(gate_is_zero(gate) ? 0.f : x);
         };
         put(n, s + before + all);
         put(n + 1, d1 + behind + (before + t0) + all);
